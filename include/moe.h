@@ -294,6 +294,130 @@ moe_status moe_latent_layer_timed(const moe_latent_desc *desc, const uint16_t *x
                                   uint16_t *out_bf16, float *out_f32, int32_t out_mode,
                                   void *ws, size_t ws_bytes, void *stream, void *const *events);
 
+/*
+ * Routing in its other usual forms, from router logits the caller computed:
+ * softmax or sigmoid scores, a selection bias, groups of experts of which
+ * only the best are considered, top-k, renormalised and scaled weights.
+ *
+ *   score:   s_e = 1 / (1 + exp(-l_e))                       (MOE_SCORE_SIGMOID)
+ *            s_e = exp(l_e) / sum_i exp(l_i)                 (MOE_SCORE_SOFTMAX)
+ *   chosen by c_e = s_e + bias_e (the bias steers selection only);
+ *   groups:  expert e is in group e / (E / n_groups); a group's value is its
+ *            largest c (MOE_GROUP_MAX) or the sum of its two largest
+ *            (MOE_GROUP_TOP2; of its only one where it has no second); the
+ *            top_groups groups of the largest values stay, ties to the lower
+ *            group;
+ *   top-k:   the k experts of the largest c in them, descending, ties to the
+ *            lower id;
+ *   weight_j = s[id_j] / sum_j s[id_j] (if renorm; 0 if that sum is 0)
+ *              * routed_scale.
+ *
+ * Scores, selection and weights are computed in 64 bits, the weights rounded
+ * to fp32 once, so two experts tie only where their c are equal as doubles.
+ *
+ * An expert whose logit or bias is -inf takes no part: not in the softmax's
+ * sum, not in its group's value, never chosen.  Where fewer than k experts
+ * are left the remaining places hold id -1 and weight 0 (moe_expert_forward
+ * drops such terms).  A logit of +inf is the limit (softmax: the experts at
+ * +inf share the whole).  A NaN logit makes its own score NaN (softmax: every
+ * score of its token); a NaN c ranks with +inf, so it is chosen and its NaN
+ * weight shows.
+ */
+typedef enum { MOE_BF16 = 0, MOE_F16 = 1, MOE_F32 = 2 } moe_type;
+typedef enum { MOE_SCORE_SIGMOID = 0, MOE_SCORE_SOFTMAX = 1 } moe_score;
+typedef enum { MOE_GROUP_MAX = 0, MOE_GROUP_TOP2 = 1 } moe_group_score;
+
+/* Supported: 1 <= top_k <= E <= 1024, top_k <= 64, n_groups <= 64; E a
+ * multiple of n_groups, 1 <= top_groups <= n_groups and top_k <= the experts
+ * of top_groups groups (otherwise MOE_EINVAL). */
+typedef struct {
+    int32_t n_experts, top_k;
+    int32_t score;               /* moe_score                                    */
+    int32_t n_groups, top_groups;/* 1, 1: no groups                              */
+    int32_t group_score;         /* moe_group_score                              */
+    int32_t renorm;              /* 1: weights renormalised to sum to 1          */
+    float routed_scale;          /* multiplies every weight                      */
+    const float *bias;           /* [E] fp32 selection bias, or NULL for none    */
+} moe_gate_desc;
+
+/*
+ * logits: T rows of E values of logits_type (moe_type), row t at
+ * logits + t * ld (ld in elements, >= E; element alignment is enough).
+ * ids, weights: [T][k]; counts: [E] or NULL, as moe_route writes them.
+ * Needs no workspace.  The same call always gives the same bits.
+ */
+moe_status moe_gate(const moe_gate_desc *gate, const void *logits, int32_t logits_type,
+                    int64_t ld, int32_t T, int32_t *ids, float *weights, int32_t *counts,
+                    void *stream);
+
+/*
+ * moe_route with the scores, groups, bias, renormalisation and scale of
+ * `gate` (desc's own router_bias, renorm and routed_scale are not read):
+ * the fp32 logits of x with desc->router_w, computed as moe_route does, then
+ * moe_gate on them.  gate and desc have to agree on n_experts and top_k.
+ * Workspace as for moe_route.
+ */
+moe_status moe_route_gated(const moe_layer_desc *desc, const moe_gate_desc *gate,
+                           const uint16_t *x, int32_t T, int32_t *ids, float *weights,
+                           int32_t *counts, void *ws, size_t ws_bytes, void *stream);
+
+/*
+ * Dense product with its epilogue, for the layers around the experts (router
+ * logits, projections, dense and shared FFNs):
+ *
+ *   a[t][n] = sum_k x[t][k] * w[n][k] + bias[n]
+ *   u[t][n] = sum_k x[t][k] * w_up[n][k] + bias_up[n]    (gated activations)
+ *   out[t][n] = act(a[t][n] (, u[t][n])) + residual[t][n]
+ *
+ *   MOE_LINEAR_NONE a, RELU max(a, 0), SILU a sigmoid(a),
+ *   GELU a Phi(a) = a erfc(-a / sqrt 2) / 2,
+ *   GELU_TANH a (1 + tanh(sqrt(2 / pi) (a + 0.044715 a^3))) / 2,
+ *   gated: SITU_GLU and SWIGLU, moe_act's SiTU-GLU and SwiGLU of (a, u).
+ *
+ * x, w, w_up and the 16-bit output have desc->type (MOE_BF16 or MOE_F16);
+ * the sums, the epilogue and the fp32 output are fp32, the 16-bit output one
+ * round to nearest even of it.  A single token takes the same call.
+ */
+typedef enum {
+    MOE_LINEAR_NONE = 0, MOE_LINEAR_RELU = 1, MOE_LINEAR_SILU = 2, MOE_LINEAR_GELU = 3,
+    MOE_LINEAR_GELU_TANH = 4, MOE_LINEAR_SITU_GLU = 5, MOE_LINEAR_SWIGLU = 6
+} moe_linear_act;
+
+/* Supported: 1 <= n_in, n_out <= 2^20, n_in <= ldw <= 2^22.  Elements need
+ * their own alignment only; rows that are 16-byte aligned (pointers and
+ * leading dimensions) with n_in a multiple of 8 take the faster kernels. */
+typedef struct {
+    int32_t n_in, n_out;
+    int32_t type;            /* moe_type of x, w, w_up and the 16-bit output      */
+    int32_t act;             /* moe_linear_act                                   */
+    float situ_b1, situ_b2;  /* SiTU betas; unused otherwise                      */
+    int32_t bias_type;       /* MOE_F32 or `type`                                */
+    int32_t residual_type;   /* MOE_F32 or `type`                                */
+    int64_t ldw;             /* elements between rows of w and of w_up            */
+    const void *w;           /* [n_out][n_in]                                    */
+    const void *w_up;        /* [n_out][n_in], for the gated activations only     */
+    const void *bias;        /* [n_out], or NULL                                 */
+    const void *bias_up;     /* [n_out], or NULL (gated activations only)         */
+} moe_linear_desc;
+
+/* Workspace bytes of moe_linear for up to max_tokens tokens (0 if the
+ * descriptor is invalid or unsupported); 256-byte aligned, no initialisation
+ * needed, nothing in it a caller reads. */
+size_t moe_linear_workspace_bytes(const moe_linear_desc *desc, int32_t max_tokens);
+
+/*
+ * x: T rows of n_in values, ldx (n_in .. 2^22) elements apart.  residual:
+ * NULL, or T rows of n_out values, ldr elements apart, ldr >= n_out or 0 (the
+ * same row for every token).  out_mode: MOE_OUT_BF16 writes out_half (the
+ * 16-bit output, in desc->type), MOE_OUT_F32 out_f32, MOE_OUT_BOTH both; rows
+ * ldo >= n_out elements apart, the elements between them left as they are.
+ * An output may be the residual's own buffer (same pointer, row distance and
+ * type); otherwise outputs must not overlap inputs.
+ */
+moe_status moe_linear(const moe_linear_desc *desc, const void *x, int64_t ldx, int32_t T,
+                      const void *residual, int64_t ldr, void *out_half, float *out_f32,
+                      int64_t ldo, int32_t out_mode, void *ws, size_t ws_bytes, void *stream);
+
 /* Static text for a status code. */
 const char *moe_status_str(int32_t status);
 

@@ -21,11 +21,18 @@ OK, EINVAL, EUNSUPPORTED, EWORKSPACE, EHIP = 0, -1, -2, -3, -4
 ACT_SITU, ACT_SWIGLU = 0, 1
 OUT_BF16, OUT_F32, OUT_BOTH = 0, 1, 2
 PATH_AUTO, PATH_GEMV, PATH_MFMA = 0, 1, 2
+OUT_HALF = OUT_BF16  # moe_linear: the 16-bit output, in the descriptor's type
+BF16, F16, F32 = 0, 1, 2
+SCORE_SIGMOID, SCORE_SOFTMAX = 0, 1
+GROUP_MAX, GROUP_TOP2 = 0, 1
+(LINEAR_NONE, LINEAR_RELU, LINEAR_SILU, LINEAR_GELU, LINEAR_GELU_TANH, LINEAR_SITU_GLU,
+ LINEAR_SWIGLU) = range(7)
 
 EXPORTS = ("moe_workspace_bytes", "moe_path_for", "moe_route", "moe_expert_forward",
            "moe_layer", "moe_layer_noalloc", "moe_layer_timed", "moe_set_one_token_router_wait",
            "moe_latent_workspace_bytes", "moe_latent_path_for", "moe_latent_layer",
-           "moe_latent_layer_timed", "moe_status_str")
+           "moe_latent_layer_timed", "moe_gate", "moe_route_gated", "moe_linear_workspace_bytes",
+           "moe_linear", "moe_status_str")
 TIMED_EVENTS = 6
 NOALLOC_WS_BYTES = 128 << 20  # MOE_NOALLOC_WS_BYTES: the static workspace of moe_layer_noalloc
 
@@ -71,6 +78,27 @@ class LatentDesc(ctypes.Structure):
     ]
 
 
+class GateDesc(ctypes.Structure):
+    """Mirror of moe_gate_desc."""
+    _fields_ = [
+        ("n_experts", ctypes.c_int32), ("top_k", ctypes.c_int32), ("score", ctypes.c_int32),
+        ("n_groups", ctypes.c_int32), ("top_groups", ctypes.c_int32),
+        ("group_score", ctypes.c_int32), ("renorm", ctypes.c_int32),
+        ("routed_scale", ctypes.c_float), ("bias", ctypes.c_void_p),
+    ]
+
+
+class LinearDesc(ctypes.Structure):
+    """Mirror of moe_linear_desc."""
+    _fields_ = [
+        ("n_in", ctypes.c_int32), ("n_out", ctypes.c_int32), ("type", ctypes.c_int32),
+        ("act", ctypes.c_int32), ("situ_b1", ctypes.c_float), ("situ_b2", ctypes.c_float),
+        ("bias_type", ctypes.c_int32), ("residual_type", ctypes.c_int32), ("ldw", ctypes.c_int64),
+        ("w", ctypes.c_void_p), ("w_up", ctypes.c_void_p),
+        ("bias", ctypes.c_void_p), ("bias_up", ctypes.c_void_p),
+    ]
+
+
 _lib = None
 
 
@@ -109,6 +137,16 @@ def lib() -> ctypes.CDLL:
         L.moe_latent_layer_timed.argtypes = [PL, vp, i32, vp, vp, i32, vp, sz, vp, ctypes.POINTER(vp)]
         L.moe_set_one_token_router_wait.restype = i32
         L.moe_set_one_token_router_wait.argtypes = [i32]
+        i64 = ctypes.c_int64
+        L.moe_gate.restype = i32
+        L.moe_gate.argtypes = [ctypes.POINTER(GateDesc), vp, i32, i64, i32, vp, vp, vp, vp]
+        L.moe_route_gated.restype = i32
+        L.moe_route_gated.argtypes = [P, ctypes.POINTER(GateDesc), vp, i32, vp, vp, vp, vp, sz, vp]
+        L.moe_linear_workspace_bytes.restype = sz
+        L.moe_linear_workspace_bytes.argtypes = [ctypes.POINTER(LinearDesc), i32]
+        L.moe_linear.restype = i32
+        L.moe_linear.argtypes = [ctypes.POINTER(LinearDesc), vp, i64, i32, vp, i64, vp, vp, i64, i32,
+                                 vp, sz, vp]
         L.moe_status_str.restype = ctypes.c_char_p
         L.moe_status_str.argtypes = [i32]
         _lib = L
@@ -304,3 +342,151 @@ def make_latent_desc(n_experts: int, top_k: int, hidden: int, latent: int, d_ffn
                  "w2_s", "norm_w", "up", "sh_w1", "sh_w3", "sh_w2"):
         setattr(d, name, _ptr(tensors.get(name)))
     return d
+
+
+# -------------------------------------------- routing from logits, dense product
+
+_types = None
+
+
+def _type_of(t) -> int:
+    """moe_type of a tensor's dtype."""
+    global _types
+    if _types is None:
+        import torch
+        _types = {torch.bfloat16: BF16, torch.float16: F16, torch.float32: F32}
+    try:
+        return _types[t.dtype]
+    except KeyError:
+        raise MoeError(EINVAL, f"dtype {t.dtype}") from None
+
+
+def _rows(t, rows: int, cols: int, what: str) -> int:
+    """Elements between the rows of a tensor of at least `rows` rows of `cols` contiguous values."""
+    shape, stride = t.shape, t.stride()
+    if len(shape) != 2 or shape[0] < rows or shape[1] != cols or (stride[1] != 1 and cols > 1):
+        raise MoeError(EINVAL, f"{what}: {rows} rows of {cols} contiguous values wanted, got {tuple(shape)}, strides {tuple(stride)}")
+    return stride[0] if rows > 1 else max(stride[0], cols)
+
+
+def _same_device(first, *others) -> None:
+    for t in others:
+        if t is not None and t.device != first.device:
+            raise MoeError(EINVAL, f"tensors on {first.device} and {t.device}")
+
+
+def _call(x, stream, f, *args) -> int:
+    """f(*args, stream) on x's device: that device's current stream where none is given."""
+    import torch
+    i = x.device.index
+    if i != torch.cuda.current_device():
+        with torch.cuda.device(i):
+            return f(*args, _stream(stream))
+    return f(*args, _stream(stream))
+
+
+def _flat(t, n: int, dtype: str, what: str):
+    """The address of n contiguous values of that dtype, or None."""
+    if t is None:
+        return None
+    if t.numel() < n or not t.is_contiguous() or str(t.dtype) != dtype:
+        raise MoeError(EINVAL, f"{what}: {n} contiguous {dtype} values wanted, got {tuple(t.shape)} {t.dtype}")
+    return t.data_ptr()
+
+
+def make_gate_desc(n_experts: int, top_k: int, score: int = SCORE_SIGMOID, bias=None,
+                   n_groups: int = 1, top_groups: int = 1, group_score: int = GROUP_MAX,
+                   renorm: int = 1, routed_scale: float = 1.0) -> GateDesc:
+    """Fill a gate descriptor; bias: a float32 tensor of n_experts values, or None.  The
+    descriptor holds its address only: keep the tensor."""
+    d = GateDesc()
+    d.n_experts, d.top_k, d.score = n_experts, top_k, score
+    d.n_groups, d.top_groups, d.group_score = n_groups, top_groups, group_score
+    d.renorm, d.routed_scale = renorm, routed_scale
+    d.bias = _flat(bias, n_experts, "torch.float32", "bias")
+    return d
+
+
+def gate(desc: GateDesc, logits, T: int, ids, weights, counts=None, stream=None) -> None:
+    """moe_gate on the first T rows of logits ([.., n_experts], float32, bfloat16 or float16;
+    rows may be apart)."""
+    E, n = desc.n_experts, T * desc.top_k
+    _same_device(logits, ids, weights, counts)
+    _check(_call(logits, stream, lib().moe_gate, ctypes.byref(desc), logits.data_ptr(), _type_of(logits),
+                 _rows(logits, T, E, "logits"), T, _flat(ids, n, "torch.int32", "ids"),
+                 _flat(weights, n, "torch.float32", "weights"), _flat(counts, E, "torch.int32", "counts")),
+           "moe_gate")
+
+
+def route_gated(desc: LayerDesc, gate_desc: GateDesc, x, T: int, ids, weights, counts, ws,
+                stream=None) -> None:
+    wp, wn = _ws(ws)
+    _check(lib().moe_route_gated(ctypes.byref(desc), ctypes.byref(gate_desc), _ptr(x), T, _ptr(ids),
+                                 _ptr(weights), _ptr(counts), wp, wn, _stream(stream)), "moe_route_gated")
+
+
+def make_linear_desc(w, w_up=None, bias=None, bias_up=None, act: int = LINEAR_NONE,
+                     situ_b1: float = 4.0, situ_b2: float = 25.0,
+                     residual_type: Optional[int] = None) -> LinearDesc:
+    """Fill a product's descriptor from w [n_out][n_in] (bfloat16 or float16; rows may be apart),
+    w_up like it for a gated act, biases [n_out] of w's dtype or float32; residual_type: F32, or
+    None for w's.  The descriptor holds addresses only: keep the tensors."""
+    d = LinearDesc()
+    n, k = w.shape
+    d.n_in, d.n_out, d.type, d.act = k, n, _type_of(w), act
+    d.situ_b1, d.situ_b2 = situ_b1, situ_b2
+    if d.type == F32:
+        raise MoeError(EINVAL, f"w: {w.dtype}")
+    d.ldw = _rows(w, n, k, "w")
+    _same_device(w, w_up, bias, bias_up)
+    if w_up is not None and (w_up.dtype != w.dtype or _rows(w_up, n, k, "w_up") != d.ldw or w_up.shape != w.shape):
+        raise MoeError(EINVAL, "w_up: not laid out as w")
+    b = bias if bias is not None else bias_up
+    d.bias_type = d.type if b is None else _type_of(b)
+    d.residual_type = d.type if residual_type is None else residual_type
+    d.w, d.w_up = w.data_ptr(), None if w_up is None else w_up.data_ptr()
+    d.bias = _flat(bias, n, str(b.dtype) if b is not None else "", "bias")
+    d.bias_up = _flat(bias_up, n, str(b.dtype) if b is not None else "", "bias_up")
+    return d
+
+
+def linear_workspace_bytes(desc: LinearDesc, max_tokens: int) -> int:
+    return int(lib().moe_linear_workspace_bytes(ctypes.byref(desc), max_tokens))
+
+
+def linear_workspace(desc: LinearDesc, max_tokens: int, device="cuda"):
+    """An uninitialised workspace (uint8 tensor) for products of up to max_tokens tokens."""
+    import torch
+    n = linear_workspace_bytes(desc, max_tokens)
+    if n == 0:
+        raise MoeError(EINVAL, "moe_linear_workspace_bytes: invalid or unsupported descriptor")
+    return torch.empty(n, dtype=torch.uint8, device=device)
+
+
+def linear(desc: LinearDesc, x, T: int, out_half, out_f32, out_mode: int, ws, residual=None,
+           stream=None) -> None:
+    """moe_linear on the first T rows of x; residual: [.., n_out] of the descriptor's residual
+    type (one expanded row: the same for every token).  Two outputs have the same row distance."""
+    n, half = desc.n_out, desc.type
+    if _type_of(x) != half:
+        raise MoeError(EINVAL, f"x: {x.dtype}")
+    _same_device(x, out_half, out_f32, residual)
+    ldo = ldr = op = fp = rp = None
+    if out_mode != OUT_F32 and out_half is not None:
+        if _type_of(out_half) != half:
+            raise MoeError(EINVAL, f"out_half: {out_half.dtype}")
+        ldo, op = _rows(out_half, T, n, "out_half"), out_half.data_ptr()
+    if out_mode != OUT_HALF and out_f32 is not None:
+        if _type_of(out_f32) != F32:
+            raise MoeError(EINVAL, f"out_f32: {out_f32.dtype}")
+        ld, fp = _rows(out_f32, T, n, "out_f32"), out_f32.data_ptr()
+        if ldo is not None and ld != ldo:
+            raise MoeError(EINVAL, "outputs with different row distances")
+        ldo = ld
+    if residual is not None:
+        if _type_of(residual) != desc.residual_type:
+            raise MoeError(EINVAL, f"residual: {residual.dtype}")
+        ldr, rp = _rows(residual, T, n, "residual"), residual.data_ptr()
+    wp, wn = _ws(ws)
+    _check(_call(x, stream, lib().moe_linear, ctypes.byref(desc), x.data_ptr(), _rows(x, T, desc.n_in, "x"), T,
+                 rp, ldr or 0, op, fp, n if ldo is None else ldo, out_mode, wp, wn), "moe_linear")

@@ -18,6 +18,7 @@ constexpr int kMaxExperts = 1024;  // router top-k keeps E/64 scores per lane
 constexpr int kMaxTopK = 64;
 constexpr int kMaxDim = 4096;      // d and F: GEMV lanes hold <= 2 MXFP4 blocks
 constexpr int kMaxShared = 8;
+constexpr int kMaxGroups = 64;     // moe_gate: one lane per group of experts
 constexpr size_t kWsControlBytes = 13 * 1024;  // workspace bytes [0, this): the one-token control block
 constexpr int kDispatchTokens = 64;  // tokens per dispatch block (one 64-bit mask)
 
@@ -523,5 +524,39 @@ hipError_t launch_decode1(const Shape &s, const uint16_t *x, const Weights &wt, 
                           int do_topk, int32_t *ids, float *wts, int32_t *counts_out, int shared,
                           const Work &w, uint16_t *out_bf16, float *out_f32, hipStream_t stream,
                           hipEvent_t const *ev2, const float *zsc = nullptr);
+
+// ---- routing from given logits (moe_gate) and the dense product (moe_linear)
+
+struct GateParams {
+    int T, E, k;
+    int softmax, groups, top_groups, top2, renorm;
+    uint32_t group_inv;   // ceil(2^20 / (E / groups)): e * group_inv >> 20 is e's group for e < 1024
+    float scale;
+    const void *logits;
+    int64_t ld;
+    const float *bias;
+    int32_t *ids;
+    float *weights;
+    int32_t *counts;
+};
+// logits_type: moe_type
+hipError_t launch_gate(const GateParams &p, int logits_type, hipStream_t st);
+
+struct LinearParams {
+    int M, N, K;          // tokens, outputs, inputs
+    int act;              // moe_linear_act
+    float b1, b2;
+    const void *x, *w, *w_up;
+    int64_t ldx, ldw;
+    const void *bias, *bias_up, *res;
+    int bias_f32, res_f32;
+    int64_t ldr;
+    void *out_half;
+    float *out_f32;
+    int64_t ldo;
+    float *part;          // workspace
+};
+size_t linear_workspace(const LinearParams &p);
+hipError_t launch_linear(const LinearParams &p, bool f16, hipStream_t st);
 
 }  // namespace moe

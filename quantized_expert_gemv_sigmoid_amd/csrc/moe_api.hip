@@ -189,6 +189,15 @@ hipError_t mark(hipEvent_t const *ev, int i, hipStream_t st)
     return ev ? hipEventRecord(ev[i], st) : hipSuccess;
 }
 
+// the fp32 router logits of every token into w.logits
+hipError_t run_router_logits(const moe_layer_desc *d, const Shape &s, const uint16_t *x, const Work &w,
+                             hipStream_t st)
+{
+    if (path_of(d, s.T) == MOE_PATH_MFMA && s.T > kFrontRouterMaxTokens)
+        return moe::launch_mfma_router(s, x, weights_of(d), w, st);
+    return moe::launch_front(s, x, weights_of(d), 1, 0, w, st);
+}
+
 // The launch sequence shared by every entry point:
 //   front    router logits (do_router) + shared experts' gate/up (GEMV path)
 //   dispatch top-k (do_topk) + histogram / scan / permutation
@@ -449,6 +458,93 @@ moe_status run_latent(const moe_latent_desc *d, int32_t T, const uint16_t *x, in
     return MOE_OK;
 }
 
+// --------------------------------------------- routing from logits, products
+
+moe_status check_gate(const moe_gate_desc *g)
+{
+    if (!g) return MOE_EINVAL;
+    if (g->n_experts < 1 || g->top_k < 1 || g->top_k > g->n_experts) return MOE_EINVAL;
+    if (g->score != MOE_SCORE_SIGMOID && g->score != MOE_SCORE_SOFTMAX) return MOE_EINVAL;
+    if (g->group_score != MOE_GROUP_MAX && g->group_score != MOE_GROUP_TOP2) return MOE_EINVAL;
+    if (g->renorm != 0 && g->renorm != 1) return MOE_EINVAL;
+    if (!isfinite(g->routed_scale)) return MOE_EINVAL;
+    if (g->bias && !aligned(g->bias, 4)) return MOE_EINVAL;
+    if (g->n_groups < 1 || g->n_experts % g->n_groups || g->top_groups < 1 || g->top_groups > g->n_groups)
+        return MOE_EINVAL;
+    if (g->top_k > g->n_experts / g->n_groups * g->top_groups) return MOE_EINVAL;
+    if (g->n_experts > moe::kMaxExperts || g->top_k > moe::kMaxTopK || g->n_groups > moe::kMaxGroups)
+        return MOE_EUNSUPPORTED;
+    return MOE_OK;
+}
+
+moe::GateParams gate_params(const moe_gate_desc *g, const void *logits, int64_t ld, int32_t T, int32_t *ids,
+                            float *weights, int32_t *counts)
+{
+    moe::GateParams p;
+    p.T = T;
+    p.E = g->n_experts;
+    p.k = g->top_k;
+    p.softmax = g->score == MOE_SCORE_SOFTMAX;
+    p.groups = g->top_groups < g->n_groups ? g->n_groups : 1;  // (every group stays: no groups)
+    p.top_groups = g->top_groups;
+    p.top2 = g->group_score == MOE_GROUP_TOP2;
+    p.renorm = g->renorm;
+    const uint32_t size = (uint32_t)(g->n_experts / p.groups);
+    p.group_inv = ((1u << 20) + size - 1) / size;
+    p.scale = g->routed_scale;
+    p.logits = logits;
+    p.ld = ld;
+    p.bias = g->bias;
+    p.ids = ids;
+    p.weights = weights;
+    p.counts = counts;
+    return p;
+}
+
+constexpr int32_t kMaxLinear = 1 << 20;  // n_in, n_out
+constexpr int64_t kMaxLd = 1 << 22;      // a tile's rows stay below 4 GiB from its first
+
+bool linear_gated(int32_t act) { return act == MOE_LINEAR_SITU_GLU || act == MOE_LINEAR_SWIGLU; }
+
+moe_status check_linear(const moe_linear_desc *d)
+{
+    if (!d) return MOE_EINVAL;
+    if (d->n_in < 1 || d->n_out < 1 || d->ldw < d->n_in) return MOE_EINVAL;
+    if (d->type != MOE_BF16 && d->type != MOE_F16) return MOE_EINVAL;
+    if (d->act < MOE_LINEAR_NONE || d->act > MOE_LINEAR_SWIGLU) return MOE_EINVAL;
+    if (d->act == MOE_LINEAR_SITU_GLU &&
+        !(isfinite(d->situ_b1) && isfinite(d->situ_b2) && d->situ_b1 > 0 && d->situ_b2 > 0))
+        return MOE_EINVAL;
+    if (d->bias_type != MOE_F32 && d->bias_type != d->type) return MOE_EINVAL;
+    if (d->residual_type != MOE_F32 && d->residual_type != d->type) return MOE_EINVAL;
+    const bool gated = linear_gated(d->act);
+    if (!d->w || gated != (d->w_up != nullptr) || (!gated && d->bias_up)) return MOE_EINVAL;
+    const size_t ba = d->bias_type == MOE_F32 ? 4 : 2;
+    if (!aligned(d->w, 2) || !aligned(d->w_up, 2) || !aligned(d->bias, ba) || !aligned(d->bias_up, ba))
+        return MOE_EINVAL;
+    if (d->n_in > kMaxLinear || d->n_out > kMaxLinear || d->ldw > kMaxLd) return MOE_EUNSUPPORTED;
+    return MOE_OK;
+}
+
+moe::LinearParams linear_params(const moe_linear_desc *d, int32_t T)
+{
+    moe::LinearParams p = {};
+    p.M = T;
+    p.N = d->n_out;
+    p.K = d->n_in;
+    p.act = d->act;
+    p.b1 = d->situ_b1;
+    p.b2 = d->situ_b2;
+    p.w = d->w;
+    p.w_up = d->w_up;
+    p.ldw = d->ldw;
+    p.bias = d->bias;
+    p.bias_up = d->bias_up;
+    p.bias_f32 = d->bias_type == MOE_F32;
+    p.res_f32 = d->residual_type == MOE_F32;
+    return p;
+}
+
 constexpr int kMaxDevices = 64;
 std::atomic<void *> g_scratch_dev[kMaxDevices];
 
@@ -625,6 +721,81 @@ moe_status moe_latent_layer_timed(const moe_latent_desc *desc, const uint16_t *x
     carve_latent(desc, T, (char *)ws, &w, &b);
     return run_latent(desc, T, x, w.ids, w.wts, nullptr, w, b, out_mode, out_bf16, out_f32,
                       (hipStream_t)stream, reinterpret_cast<hipEvent_t const *>(events));
+}
+
+moe_status moe_gate(const moe_gate_desc *gate, const void *logits, int32_t logits_type, int64_t ld,
+                    int32_t T, int32_t *ids, float *weights, int32_t *counts, void *stream)
+{
+    const moe_status st = check_gate(gate);
+    if (st != MOE_OK) return st;
+    if (logits_type != MOE_BF16 && logits_type != MOE_F16 && logits_type != MOE_F32) return MOE_EINVAL;
+    if (T < 0 || ld < gate->n_experts) return MOE_EINVAL;
+    if (T > kMaxTokens) return MOE_EUNSUPPORTED;
+    if (T == 0) return MOE_OK;
+    if (!logits || !aligned(logits, logits_type == MOE_F32 ? 4 : 2)) return MOE_EINVAL;
+    if (!ids || !weights || !aligned(ids, 4) || !aligned(weights, 4) || !aligned(counts, 4)) return MOE_EINVAL;
+    (void)hipGetLastError();
+    MOE_TRY(moe::launch_gate(gate_params(gate, logits, ld, T, ids, weights, counts), logits_type,
+                             (hipStream_t)stream));
+    return MOE_OK;
+}
+
+moe_status moe_route_gated(const moe_layer_desc *desc, const moe_gate_desc *gate, const uint16_t *x,
+                           int32_t T, int32_t *ids, float *weights, int32_t *counts, void *ws,
+                           size_t ws_bytes, void *stream)
+{
+    moe_status st = check_call(desc, x, T, ws, ws_bytes);
+    if (st != MOE_OK) return st;
+    st = check_gate(gate);
+    if (st != MOE_OK) return st;
+    if (gate->n_experts != desc->n_experts || gate->top_k != desc->top_k) return MOE_EINVAL;
+    if (T == 0) return MOE_OK;
+    if (!ids || !weights || !aligned(ids, 4) || !aligned(weights, 4) || !aligned(counts, 4)) return MOE_EINVAL;
+    (void)hipGetLastError();
+    const Shape s = shape_of(desc, T);
+    Work w;
+    carve(s, (char *)ws, &w);
+    MOE_TRY(run_router_logits(desc, s, x, w, (hipStream_t)stream));
+    MOE_TRY(moe::launch_gate(gate_params(gate, w.logits, s.E, T, ids, weights, counts), MOE_F32,
+                             (hipStream_t)stream));
+    return MOE_OK;
+}
+
+size_t moe_linear_workspace_bytes(const moe_linear_desc *desc, int32_t max_tokens)
+{
+    if (check_linear(desc) != MOE_OK || max_tokens < 0 || max_tokens > kMaxTokens) return 0;
+    return moe::linear_workspace(linear_params(desc, max_tokens));
+}
+
+moe_status moe_linear(const moe_linear_desc *desc, const void *x, int64_t ldx, int32_t T,
+                      const void *residual, int64_t ldr, void *out_half, float *out_f32, int64_t ldo,
+                      int32_t out_mode, void *ws, size_t ws_bytes, void *stream)
+{
+    const moe_status st = check_linear(desc);
+    if (st != MOE_OK) return st;
+    if (T < 0 || ldx < desc->n_in || ldo < desc->n_out) return MOE_EINVAL;
+    if (residual && ldr != 0 && ldr < desc->n_out) return MOE_EINVAL;
+    if (out_mode != MOE_OUT_BF16 && out_mode != MOE_OUT_F32 && out_mode != MOE_OUT_BOTH) return MOE_EINVAL;
+    if (T > kMaxTokens || ldx > kMaxLd || ldo > kMaxLd || (residual && ldr > kMaxLd)) return MOE_EUNSUPPORTED;
+    if (T == 0) return MOE_OK;
+    if (!x || !aligned(x, 2)) return MOE_EINVAL;
+    if (residual && !aligned(residual, desc->residual_type == MOE_F32 ? 4 : 2)) return MOE_EINVAL;
+    if (out_mode != MOE_OUT_F32 && (!out_half || !aligned(out_half, 2))) return MOE_EINVAL;
+    if (out_mode != MOE_OUT_BF16 && (!out_f32 || !aligned(out_f32, 4))) return MOE_EINVAL;
+    if (!ws || !aligned(ws, 256)) return MOE_EINVAL;
+    moe::LinearParams p = linear_params(desc, T);
+    if (ws_bytes < moe::linear_workspace(p)) return MOE_EWORKSPACE;
+    (void)hipGetLastError();
+    p.x = x;
+    p.ldx = ldx;
+    p.res = residual;
+    p.ldr = ldr;
+    p.out_half = out_mode != MOE_OUT_F32 ? out_half : nullptr;
+    p.out_f32 = out_mode != MOE_OUT_BF16 ? out_f32 : nullptr;
+    p.ldo = ldo;
+    p.part = (float *)ws;
+    MOE_TRY(moe::launch_linear(p, desc->type == MOE_F16, (hipStream_t)stream));
+    return MOE_OK;
 }
 
 const char *moe_status_str(int32_t status)

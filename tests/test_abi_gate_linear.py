@@ -1,0 +1,188 @@
+"""Host-side checks of moe_gate, moe_route_gated and moe_linear: descriptor layouts, and arguments refused before any
+launch (no GPU needed)."""
+import ctypes
+import os
+import subprocess
+
+import pytest
+
+import quantized_expert_gemv_sigmoid_amd as moe
+from test_abi import FAKE, ROOT, desc as layer_desc
+
+torch = pytest.importorskip("torch")
+
+
+@pytest.fixture(scope="module")
+def L():
+    if not os.path.exists(moe.LIB_PATH):
+        from quantized_expert_gemv_sigmoid_amd import build
+        build.build()
+    return moe.lib()
+
+
+@pytest.mark.parametrize("mirror,name", [(moe.GateDesc, "moe_gate_desc"), (moe.LinearDesc, "moe_linear_desc")])
+def test_layout_matches_c(tmp_path, mirror, name):
+    fields = [f for f, _ in mirror._fields_]
+    prog = tmp_path / "layout.c"
+    prog.write_text('#include <stdio.h>\n#include <stddef.h>\n#include "moe.h"\nint main(void){ printf("%zu\\n", '
+                    f"sizeof({name}));\n" + "\n".join(f'printf("%zu\\n", offsetof({name}, {f}));' for f in fields) +
+                    "\nreturn 0; }\n")
+    exe = tmp_path / "layout"
+    subprocess.check_call(["gcc", "-std=c11", "-I", os.path.join(ROOT, "include"), str(prog), "-o", str(exe)])
+    vals = [int(v) for v in subprocess.check_output([str(exe)]).split()]
+    assert vals[0] == ctypes.sizeof(mirror)
+    assert vals[1:] == [getattr(mirror, f).offset for f in fields]
+
+
+def gate_desc(**kw):
+    d = moe.make_gate_desc(896, 16)
+    d.bias = FAKE
+    for k, v in kw.items():
+        setattr(d, k, v)
+    return d
+
+
+def call_gate(L, d, logits=FAKE, type=moe.F32, ld=896, T=2, ids=FAKE, weights=FAKE, counts=None):
+    return L.moe_gate(ctypes.byref(d) if d is not None else None, logits, type, ld, T, ids, weights, counts, None)
+
+
+@pytest.mark.parametrize("kw,status", [
+    (dict(n_experts=0), moe.EINVAL),
+    (dict(top_k=0), moe.EINVAL),
+    (dict(top_k=897), moe.EINVAL),
+    (dict(score=2), moe.EINVAL),
+    (dict(group_score=-1), moe.EINVAL),
+    (dict(renorm=2), moe.EINVAL),
+    (dict(routed_scale=float("nan")), moe.EINVAL),
+    (dict(bias=FAKE + 2), moe.EINVAL),
+    (dict(n_groups=0), moe.EINVAL),
+    (dict(n_groups=5), moe.EINVAL),                      # 896 experts are no five groups
+    (dict(n_groups=8, top_groups=0), moe.EINVAL),
+    (dict(n_groups=8, top_groups=9), moe.EINVAL),
+    (dict(n_groups=64, top_groups=1), moe.EINVAL),       # 14 experts left for 16 places
+    (dict(n_groups=128, top_groups=128), moe.EUNSUPPORTED),
+    (dict(n_experts=1025), moe.EUNSUPPORTED),
+    (dict(top_k=65), moe.EUNSUPPORTED),
+])
+def test_gate_descriptor_refused(L, kw, status):
+    assert call_gate(L, gate_desc(**kw), ld=4096) == status
+
+
+def test_gate_call_refused(L):
+    d = gate_desc()
+    assert call_gate(L, None) == moe.EINVAL
+    assert call_gate(L, d, T=0, logits=None) == moe.OK
+    for kw in (dict(T=-1), dict(ld=895), dict(type=3), dict(logits=None), dict(logits=FAKE + 2), dict(ids=None),
+               dict(weights=None), dict(ids=FAKE + 2), dict(counts=FAKE + 1), dict(type=moe.BF16, logits=FAKE + 1)):
+        assert call_gate(L, d, **kw) == moe.EINVAL, kw
+    assert call_gate(L, d, T=(1 << 20) + 1) == moe.EUNSUPPORTED
+
+
+def test_route_gated_refused(L):
+    d = layer_desc()
+    need = L.moe_workspace_bytes(ctypes.byref(d), 2)
+
+    def call(g, T=2, ws=(FAKE * 16, need), ids=FAKE, x=FAKE, d=d):
+        return L.moe_route_gated(ctypes.byref(d), ctypes.byref(g) if g is not None else None, x, T, ids, FAKE, None,
+                                 ws[0], ws[1], None)
+
+    assert call(None) == moe.EINVAL
+    assert call(gate_desc(top_k=8)) == moe.EINVAL
+    assert call(gate_desc(n_experts=512)) == moe.EINVAL
+    assert call(gate_desc(score=5)) == moe.EINVAL
+    assert call(gate_desc(), ids=None) == moe.EINVAL
+    assert call(gate_desc(), x=None) == moe.EINVAL
+    assert call(gate_desc(), ws=(FAKE * 16, need - 1)) == moe.EWORKSPACE
+    assert call(gate_desc(), T=0) == moe.OK
+    assert call(gate_desc(), d=layer_desc(top_k=80)) == moe.EUNSUPPORTED
+
+
+def linear_desc(**kw):
+    d = moe.LinearDesc()
+    d.n_in, d.n_out, d.ldw, d.type, d.act = 640, 512, 640, moe.BF16, moe.LINEAR_NONE
+    d.situ_b1, d.situ_b2, d.bias_type, d.residual_type = 4.0, 25.0, moe.F32, moe.BF16
+    d.w = FAKE
+    for k, v in kw.items():
+        setattr(d, k, v)
+    return d
+
+
+def call_linear(L, d, x=FAKE, ldx=640, T=3, res=None, ldr=0, oh=FAKE, of=None, ldo=512, mode=moe.OUT_HALF,
+                ws=(FAKE * 16, 1 << 40)):
+    return L.moe_linear(ctypes.byref(d) if d is not None else None, x, ldx, T, res, ldr, oh, of, ldo, mode, ws[0],
+                        ws[1], None)
+
+
+@pytest.mark.parametrize("kw,status", [
+    (dict(n_in=0), moe.EINVAL),
+    (dict(n_out=0), moe.EINVAL),
+    (dict(ldw=639), moe.EINVAL),
+    (dict(type=moe.F32), moe.EINVAL),
+    (dict(act=7), moe.EINVAL),
+    (dict(act=-1), moe.EINVAL),
+    (dict(bias_type=moe.F16), moe.EINVAL),
+    (dict(residual_type=moe.F16), moe.EINVAL),
+    (dict(w=None), moe.EINVAL),
+    (dict(w=FAKE + 1), moe.EINVAL),
+    (dict(w_up=FAKE), moe.EINVAL),                                   # a second matrix without a gated act
+    (dict(bias_up=FAKE), moe.EINVAL),
+    (dict(act=moe.LINEAR_SWIGLU), moe.EINVAL),                       # a gated act without it
+    (dict(act=moe.LINEAR_SITU_GLU, w_up=FAKE, situ_b1=0.0), moe.EINVAL),
+    (dict(act=moe.LINEAR_SITU_GLU, w_up=FAKE, situ_b2=float("inf")), moe.EINVAL),
+    (dict(bias=FAKE + 2), moe.EINVAL),
+    (dict(n_out=(1 << 20) + 1), moe.EUNSUPPORTED),
+    (dict(ldw=(1 << 22) + 1), moe.EUNSUPPORTED),
+])
+def test_linear_descriptor_refused(L, kw, status):
+    d = linear_desc(**kw)
+    assert call_linear(L, d, ldx=1 << 20, ldo=1 << 21) == status
+    assert L.moe_linear_workspace_bytes(ctypes.byref(d), 4) == 0
+
+
+def test_linear_call_refused(L):
+    d = linear_desc()
+    assert call_linear(L, None) == moe.EINVAL
+    assert call_linear(L, d, T=0, x=None, ws=(None, 0)) == moe.OK
+    need = L.moe_linear_workspace_bytes(ctypes.byref(d), 3)
+    assert need > 0
+    for kw in (dict(T=-1), dict(ldx=639), dict(ldo=511), dict(x=None), dict(x=FAKE + 1), dict(oh=None), dict(mode=3),
+               dict(res=FAKE, ldr=511), dict(res=FAKE, ldr=-1), dict(res=FAKE + 1, ldr=512), dict(mode=moe.OUT_F32),
+               dict(mode=moe.OUT_BOTH), dict(mode=moe.OUT_F32, of=FAKE + 2), dict(ws=(None, need)),
+               dict(ws=(FAKE * 16 + 128, need))):
+        assert call_linear(L, d, **kw) == moe.EINVAL, kw
+    assert call_linear(L, d, ws=(FAKE * 16, need - 1)) == moe.EWORKSPACE
+    assert call_linear(L, d, T=(1 << 20) + 1) == moe.EUNSUPPORTED
+    assert call_linear(L, d, ldx=(1 << 22) + 1) == moe.EUNSUPPORTED
+    assert call_linear(L, d, ldo=(1 << 22) + 1) == moe.EUNSUPPORTED
+
+
+def test_linear_workspace_grows_with_tokens(L):
+    # a workspace for up to max_tokens tokens serves every smaller call
+    for kw in (dict(), dict(n_in=7168, n_out=896, ldw=7168), dict(n_in=1 << 14, n_out=64, ldw=1 << 14),
+               dict(act=moe.LINEAR_SWIGLU, w_up=FAKE), dict(n_in=5, n_out=7, ldw=5)):
+        d = linear_desc(**kw)
+        sizes = [L.moe_linear_workspace_bytes(ctypes.byref(d), T) for T in range(0, 1200, 7)]
+        assert sizes[0] > 0 and sizes == sorted(sizes)
+
+
+def test_binding_refuses_mismatched_tensors(L):
+    d = moe.make_gate_desc(8, 2)
+    i, w = torch.empty(3, 2, dtype=torch.int32), torch.empty(3, 2)
+    for logits, ids, weights in ((torch.empty(3, 9), i, w), (torch.empty(2, 8), i, w), (torch.empty(8, 3).t(), i, w),
+                                 (torch.empty(3, 8).double(), i, w), (torch.empty(3, 8), i.long(), w),
+                                 (torch.empty(3, 8), i[:2], w), (torch.empty(3, 8), i, w.half())):
+        with pytest.raises(moe.MoeError):
+            moe.gate(d, logits, 3, ids, weights)
+    with pytest.raises(moe.MoeError):
+        moe.make_gate_desc(8, 2, bias=torch.empty(7))
+    wt = torch.empty(5, 8, dtype=torch.bfloat16)
+    for kw in (dict(w=wt.float()), dict(w=wt.t()), dict(w=wt, w_up=wt[:4]), dict(w=wt, w_up=wt.half()),
+               dict(w=wt, bias=torch.empty(4)), dict(w=wt, w_up=wt, bias=torch.empty(5), bias_up=wt[:, 0])):
+        with pytest.raises(moe.MoeError):
+            moe.make_linear_desc(**kw)
+    ld = moe.make_linear_desc(wt)
+    x, o = torch.empty(3, 8, dtype=torch.bfloat16), torch.empty(3, 5, dtype=torch.bfloat16)
+    for kw in (dict(x=x.half()), dict(x=x[:, :7]), dict(out_half=o.half()), dict(out_half=o[:2]),
+               dict(residual=torch.empty(3, 5)), dict(residual=o[:, :4])):
+        with pytest.raises(moe.MoeError):
+            moe.linear(ld, **{**dict(x=x, T=3, out_half=o, out_f32=None, out_mode=moe.OUT_HALF, ws=(256, 1 << 30)), **kw})
