@@ -555,6 +555,7 @@ struct LinearParams {
     float *out_f32;
     int64_t ldo;
     float *part;          // workspace
+    int vec;              // set by launch_linear: outputs and residual take four values at a time
 };
 size_t linear_workspace(const LinearParams &p);
 hipError_t launch_linear(const LinearParams &p, bool f16, hipStream_t st);
