@@ -1,11 +1,23 @@
 // Routing from given logits: softmax or sigmoid scores, selection bias,
 // groups, top-k, renormalised weights (moe_gate).
 //
-// One wave per token: lane l holds experts l, l + 64, ...  Scores and
-// selection values are doubles, so that experts whose fp32 values would round
-// together keep their order; a value of -inf marks an expert that takes no
-// part, and a NaN one ranks as +inf.  The k picks are k rounds of a wave-wide
-// maximum.
+// One wave per token: lane l holds experts l, l + 64, ...  Selection values
+// are compared as doubles, so that experts whose fp32 values would round
+// together keep their order; but only for the few experts that can be among
+// the best k:
+//
+//   - every expert gets an fp32 value a in the order of the selection values
+//     up to a margin d: the logit itself where there is no bias (both scores
+//     grow with it), else the score in fp32 plus the bias;
+//   - t, at most the k-th largest of the lanes' maxima, is a lower bound of
+//     the k-th largest a, so the best k are among the experts with
+//     a >= t - 2 d (about 20 of 896 for k = 16), which are put one to a lane;
+//   - these get their scores as doubles, and their ranks by counting.
+//
+// Where more than 64 experts stay (equal logits), or two groups' values are
+// too close to tell apart in fp32, the token takes `whole`: all values as
+// doubles, k rounds of a wave-wide maximum.  A value of -inf marks an expert
+// that takes no part, and a NaN one ranks as +inf.
 #include <math.h>
 
 #include "common.h"
@@ -13,6 +25,8 @@
 namespace moe {
 
 namespace {
+
+constexpr int kGateWaves = 8;
 
 template <typename L>
 __device__ __forceinline__ float logit_f32(L v);
@@ -23,16 +37,67 @@ __device__ __forceinline__ float logit_f32<_Float16>(_Float16 v) { return (float
 template <>
 __device__ __forceinline__ float logit_f32<uint16_t>(uint16_t v) { return __uint_as_float((uint32_t)v << 16); }
 
-__device__ __forceinline__ double wave_max(double v)
+// exp(x) to about 2^-52: 2^n e^r with r = x - n ln 2 (ln 2 in two parts),
+// |r| <= ln(2) / 2, and e^r by its Taylor series to r^13 (the next term is
+// below 2^-57); past the doubles' range inf and 0
+__device__ __forceinline__ double exp64(double v)
 {
-#pragma unroll
-    for (int m = 32; m >= 1; m >>= 1) v = fmax(v, __shfl_xor(v, m, 64));
-    return v;
+    const double x = fmin(fmax(v, -1100.0), 1100.0);
+    const double n = rint(x * 1.4426950408889634);
+    double r = fma(n, -0.6931471803691238, x);
+    r = fma(n, -1.9082149292705877e-10, r);
+    double p = 1.0 / 6227020800.0;
+    p = fma(p, r, 1.0 / 479001600.0);
+    p = fma(p, r, 1.0 / 39916800.0);
+    p = fma(p, r, 1.0 / 3628800.0);
+    p = fma(p, r, 1.0 / 362880.0);
+    p = fma(p, r, 1.0 / 40320.0);
+    p = fma(p, r, 1.0 / 5040.0);
+    p = fma(p, r, 1.0 / 720.0);
+    p = fma(p, r, 1.0 / 120.0);
+    p = fma(p, r, 1.0 / 24.0);
+    p = fma(p, r, 1.0 / 6.0);
+    p = fma(p, r, 0.5);
+    p = fma(p, r, 1.0);
+    p = fma(p, r, 1.0);
+    return v != v ? v : ldexp(p, (int)n);
+}
+
+template <int CTRL>
+__device__ __forceinline__ float dpp_f(float old, float v)
+{
+    return __int_as_float(__builtin_amdgcn_update_dpp(__float_as_int(old), __float_as_int(v), CTRL, 0xF, 0xF, false));
+}
+__device__ __forceinline__ float wave_max(float v)
+{
+    v = fmaxf(v, dpp_f<0xB1>(v, v));   // quad_perm [1,0,3,2]
+    v = fmaxf(v, dpp_f<0x4E>(v, v));   // quad_perm [2,3,0,1]
+    v = fmaxf(v, dpp_f<0x141>(v, v));  // row_half_mirror
+    v = fmaxf(v, dpp_f<0x140>(v, v));  // row_mirror
+    v = fmaxf(v, __shfl_xor(v, 16, 64));
+    return fmaxf(v, __shfl_xor(v, 32, 64));
+}
+template <int CTRL>
+__device__ __forceinline__ double dpp_d(double v)
+{
+    const uint64_t u = __builtin_bit_cast(uint64_t, v);
+    const uint32_t lo = __builtin_amdgcn_update_dpp(0, (uint32_t)u, CTRL, 0xF, 0xF, true);
+    const uint32_t hi = __builtin_amdgcn_update_dpp(0, (uint32_t)(u >> 32), CTRL, 0xF, 0xF, true);
+    return __builtin_bit_cast(double, (uint64_t)hi << 32 | lo);
 }
 __device__ __forceinline__ double wave_sum64(double v)
 {
+    v += dpp_d<0xB1>(v);
+    v += dpp_d<0x4E>(v);
+    v += dpp_d<0x141>(v);
+    v += dpp_d<0x140>(v);
+    v += __shfl_xor(v, 16, 64);
+    return v + __shfl_xor(v, 32, 64);
+}
+__device__ __forceinline__ double wave_max64(double v)
+{
 #pragma unroll
-    for (int m = 32; m >= 1; m >>= 1) v += __shfl_xor(v, m, 64);
+    for (int m = 32; m >= 1; m >>= 1) v = fmax(v, __shfl_xor(v, m, 64));
     return v;
 }
 __device__ __forceinline__ int wave_min(int v)
@@ -41,136 +106,359 @@ __device__ __forceinline__ int wave_min(int v)
     for (int m = 32; m >= 1; m >>= 1) v = min(v, __shfl_xor(v, m, 64));
     return v;
 }
+__device__ __forceinline__ int below(uint64_t mask)  // set bits below this lane
+{
+    return (int)__builtin_amdgcn_mbcnt_hi((uint32_t)(mask >> 32), __builtin_amdgcn_mbcnt_lo((uint32_t)mask, 0u));
+}
 
-template <int EPL, typename L>
-__global__ __launch_bounds__(256) void k_gate(GateParams p)
+struct Pick {  // lane j < k: the j-th choice, id -1 where there is none
+    int id;
+    double s;
+};
+
+// the score of a logit: softmax with maximum m (of the experts that take
+// part) and the sum of exp(l - m)
+template <bool SOFT>
+__device__ __forceinline__ double score_of(float l, float m, double sum)
+{
+    // (+inf - +inf: the limit, 0)
+    if (SOFT) return exp64(l == m ? 0.0 : (double)l - (double)m) / sum;
+    return 1.0 / (1.0 + exp64(-(double)l));
+}
+
+__device__ __forceinline__ int group_of(const GateParams &p, int e) { return (int)((uint32_t)e * p.group_inv >> 20); }
+
+// LDS of a wave: every expert's value (in `choose` the groups' part, as
+// floats; in `whole`), or the candidates
+struct GateCands {
+    float2 cand[64];  // logit, id
+    double c[64];     // selection values
+    double s[64];     // scores and ids by rank
+    int id[64];
+};
+template <int EPL>
+union GateLds {
+    double v[64 * EPL];
+    GateCands n;
+};
+
+// Lane g < groups: whether group g stays, of the values v[E] in LDS.  P lanes
+// to a group: each takes every P-th of its experts, then their two largest
+// join.  `mine`: lane g's group value.
+template <typename T>
+__device__ __forceinline__ bool group_stays(const GateParams &p, const T *v, T &mine)
+{
+    const T ninf = -INFINITY;
+    const int lane = threadIdx.x & 63, size = p.E / p.groups, P = 1 << (31 - __builtin_clz(64 / p.groups));
+    const int g = lane / P;
+    T v1 = ninf, v2 = ninf;
+    if (g < p.groups) {
+        for (int j = lane % P; j < size; j += P) {
+            const T x = v[g * size + j];
+            v2 = fmax(v2, fmin(v1, x));
+            v1 = fmax(v1, x);
+        }
+    }
+    for (int d = 1; d < P; d <<= 1) {
+        const T o1 = __shfl_xor(v1, d, 64), o2 = __shfl_xor(v2, d, 64);
+        v2 = fmax(fmax(v2, o2), fmin(v1, o1));
+        v1 = fmax(v1, o1);
+    }
+    const T value = p.top2 ? v1 + (v2 == ninf ? (T)0 : v2) : v1;
+    mine = __shfl(value, min(lane * P, 63), 64);
+    int rank = 0;
+    for (int i = 0; i < p.groups; i++) {
+        const T o = __shfl(mine, i, 64);
+        rank += o > mine || (o == mine && i < lane) ? 1 : 0;
+    }
+    return lane < p.groups && rank < p.top_groups;
+}
+
+// everything as doubles in LDS, k rounds of a maximum
+template <bool SOFT, typename L>
+__device__ __forceinline__ Pick whole(const GateParams &p, const L *row, double *v, float m, double sum)
 {
     const int lane = threadIdx.x & 63;
-    const int t = blockIdx.x * 4 + (threadIdx.x >> 6);
-    if (t >= p.T) return;
-    const L *row = reinterpret_cast<const L *>(p.logits) + (size_t)t * p.ld;
     const double ninf = -INFINITY;
-    double s[EPL], c[EPL];
-    bool on[EPL];
-    float l[EPL];
-#pragma unroll
-    for (int i = 0; i < EPL; i++) {
-        const int e = lane + 64 * i, ec = min(e, p.E - 1);
-        l[i] = logit_f32<L>(row[ec]);
-        const float b = p.bias ? p.bias[ec] : 0.0f;
-        on[i] = e < p.E && l[i] != -INFINITY && b != -INFINITY;
-        c[i] = b;
+#pragma unroll 1
+    for (int e = lane; e < p.E; e += 64) {
+        const float l = logit_f32<L>(row[e]), b = p.bias ? p.bias[e] : 0.0f;
+        const double x = score_of<SOFT>(l, m, sum) + b;
+        v[e] = l != -INFINITY && b != -INFINITY ? (x != x ? (double)INFINITY : x) : ninf;
     }
-    if (p.softmax) {
-        float m = -INFINITY;
+    __builtin_amdgcn_wave_barrier();
+    uint64_t kept = ~0ull;
+    if (p.groups > 1) {
+        double value;
+        kept = __builtin_amdgcn_ballot_w64(group_stays<double>(p, v, value));
+    }
+    Pick mine = {-1, 0.0};
+    double best = ninf;  // the lane's largest, and whose it is
+    int id = 0;
+    bool look = true;
+#pragma unroll 1
+    for (int j = 0; j < p.k; j++) {
+        if (look) {
+            best = ninf;
+            for (int e = lane; e < p.E; e += 64) {
+                const double x = v[e];
+                const bool more = x > best && (p.groups == 1 || ((kept >> group_of(p, e)) & 1));  // (strict: the lower id of a tie)
+                best = more ? x : best;
+                id = more ? e : id;
+            }
+        }
+        const double top = wave_max64(best);
+        if (top == ninf) break;
+        const int first = wave_min(best == top ? id : 1 << 30);
+        if (lane == j) mine.id = first;
+        look = id == first && best == top;
+        if (look) v[first] = ninf;
+        __builtin_amdgcn_wave_barrier();
+    }
+    if (mine.id >= 0) mine.s = score_of<SOFT>(logit_f32<L>(row[mine.id]), m, sum);
+    return mine;
+}
+
+// a value near t may be off by this much, and so may the order of two
+__device__ __forceinline__ float margin(bool by_logit, float t)
+{
+    // By logit: two logits closer than this may have equal scores as doubles.
+    // Else: the fp32 score is off by less than 2^-21 (exp_hw(x) is within
+    // (1 + 1.45 |x|) 2^-23 of itself, which s (1 - s), or e^x for the
+    // softmax, takes below 2^-22; and a few roundings), the sum with the bias
+    // by its rounding.
+    return by_logit ? 4.8e-7f * fabsf(t) + 1e-9f : 4.8e-7f + 2.4e-7f * fabsf(t);
+}
+
+// The choices of one token from its logits l (a copy of row's, lane l's
+// experts l + 64 i) and their biases (-inf: no expert, or one switched off;
+// 0 without a bias).
+template <int EPL, bool SOFT, typename L>
+__device__ __forceinline__ Pick choose(const GateParams &p, const L *row, const float (&l)[EPL], const float (&bias)[EPL],
+                                       GateLds<EPL> &lds)
+{
+    const int lane = threadIdx.x & 63;
+    const float ninf = -INFINITY;
+    const bool by_logit = !p.bias && !(p.groups > 1 && p.top2);
+    GateCands &w = lds.n;
+    float a[EPL];
+    float m = ninf;
+    double sum = 1.0;
 #pragma unroll
-        for (int i = 0; i < EPL; i++) m = on[i] ? fmaxf(m, l[i]) : m;
+    for (int i = 0; i < EPL; i++) a[i] = l[i] != ninf ? bias[i] : ninf;  // (-inf: takes no part)
+    if (SOFT) {
 #pragma unroll
-        for (int d = 32; d >= 1; d >>= 1) m = fmaxf(m, __shfl_xor(m, d, 64));
-        double sum = 0.0;
+        for (int i = 0; i < EPL; i++) m = fmaxf(m, a[i] != ninf ? l[i] : ninf);
+        m = wave_max(m);
+        sum = 0.0;
 #pragma unroll
         for (int i = 0; i < EPL; i++) {
-            // (+inf - +inf: the limit, 0)
-            s[i] = on[i] ? exp(l[i] == m ? 0.0 : (double)l[i] - (double)m) : 0.0;
-            sum += s[i];
+            sum += a[i] != ninf ? exp64(l[i] == m ? 0.0 : (double)l[i] - (double)m) : 0.0;
+            __builtin_amdgcn_sched_barrier(0);  // (one after the other: few registers)
         }
         sum = wave_sum64(sum);
+        if (!by_logit) {
+            const float inv = (float)(1.0 / sum);
 #pragma unroll
-        for (int i = 0; i < EPL; i++) s[i] = s[i] / sum;
-    } else {
+            for (int i = 0; i < EPL; i++) a[i] = a[i] != ninf ? exp_hw(l[i] == m ? 0.0f : l[i] - m) * inv + a[i] : ninf;
+        }
+    } else if (!by_logit) {
 #pragma unroll
-        for (int i = 0; i < EPL; i++) s[i] = 1.0 / (1.0 + exp(-(double)l[i]));
+        for (int i = 0; i < EPL; i++) a[i] = a[i] != ninf ? sigmoid_hw(l[i]) + a[i] : ninf;
     }
 #pragma unroll
     for (int i = 0; i < EPL; i++) {
-        const double v = s[i] + c[i];
-        c[i] = on[i] ? (v != v ? (double)INFINITY : v) : ninf;
+        const float v = by_logit ? (a[i] != ninf ? l[i] : ninf) : a[i];
+        a[i] = v != v ? (float)INFINITY : v;
     }
+    // logits between which every two have different scores as doubles (the
+    // sigmoid's reach 1, and both scores 0, further out)
+    const float high = !by_logit || SOFT ? (float)INFINITY : 20.0f;
+    const float low = !by_logit ? ninf : SOFT ? m - 700.0f : -700.0f;
+
+    bool slow = false;
     if (p.groups > 1) {
-        double mine = ninf;  // lane g: the value of group g
-        for (int g = 0; g < p.groups; g++) {
-            double a = ninf, b = ninf;  // the lane's two largest
-#pragma unroll
-            for (int i = 0; i < EPL; i++) {
-                const double v = ((lane + 64 * i) * p.group_inv) >> 20 == g ? c[i] : ninf;
-                b = fmax(b, fmin(a, v));
-                a = fmax(a, v);
-            }
-            const double top = wave_max(a);
-            double value = top;
-            if (p.top2) {
-                // the second: the others' largest, and the second of the one
-                // lane that gave the first
-                const uint64_t who = __builtin_amdgcn_ballot_w64(a == top);
-                const bool first = lane == (int)__builtin_ctzll(who);
-                const double second = wave_max(first ? b : a);
-                value = top + (second == ninf ? 0.0 : second);
-            }
-            mine = lane == g ? value : mine;
-        }
-        int rank = 0;
-        for (int g = 0; g < p.groups; g++) {
-            const double o = __shfl(mine, g, 64);
-            rank += o > mine || (o == mine && g < lane) ? 1 : 0;
-        }
-        const uint64_t kept = __builtin_amdgcn_ballot_w64(lane < p.groups && rank < p.top_groups);
+        float *v = reinterpret_cast<float *>(lds.v);
 #pragma unroll
         for (int i = 0; i < EPL; i++)
-            c[i] = (kept >> (((lane + 64 * i) * p.group_inv) >> 20)) & 1 ? c[i] : ninf;
-    }
-    int my_id = -1;
-    double my_s = 0.0, total = 0.0;
-    for (int j = 0; j < p.k; j++) {
-        double best = ninf, bs = 0.0;
-        int bi = 0;
+            if (lane + 64 * i < p.E) v[lane + 64 * i] = a[i];
+        __builtin_amdgcn_wave_barrier();
+        float mine;
+        const bool keep = group_stays<float>(p, v, mine), drop = lane < p.groups && !keep;
+        const uint64_t kept = __builtin_amdgcn_ballot_w64(keep);
+        const float in = -wave_max(keep ? -mine : ninf), out = wave_max(drop ? mine : ninf);  // the last kept, the first not
+        // (two values, each the sum of up to two with a margin)
+        slow = out != ninf && (!(in - out > 4.0f * margin(by_logit, fmaxf(fabsf(in), fabsf(out)))) || out > high || in < low);
 #pragma unroll
-        for (int i = 0; i < EPL; i++) {
-            const bool more = c[i] > best;  // (strict: the lower id of a tie)
-            best = more ? c[i] : best;
-            bs = more ? s[i] : bs;
-            bi = more ? i : bi;
+        for (int i = 0; i < EPL; i++) a[i] = (kept >> (group_of(p, lane + 64 * i) & 63)) & 1 ? a[i] : ninf;
+        __builtin_amdgcn_wave_barrier();
+    }
+
+    // t: a value that at least k lanes' maxima reach (or -inf), by halving
+    // the range of those maxima
+    float t = ninf;
+    if (EPL > 1) {
+        float top = ninf;
+#pragma unroll
+        for (int i = 0; i < EPL; i++) top = fmaxf(top, a[i]);
+        float hi = wave_max(top), lo = -wave_max(top == ninf ? ninf : -top);
+        if (__builtin_popcountll(__builtin_amdgcn_ballot_w64(top != ninf)) >= p.k) {
+            t = lo;
+            for (int i = 0; i < 12; i++) {
+                const float mid = 0.5f * lo + 0.5f * hi;
+                const int n = __builtin_popcountll(__builtin_amdgcn_ballot_w64(top >= mid));
+                if (n >= p.k) lo = t = mid;
+                else hi = mid;
+                if (n == p.k) break;
+            }
+            t = fminf(t, high);
+            if (t < INFINITY) t -= 2.0f * margin(by_logit, t);
+            if (t < low) t = ninf;
         }
-        const double top = wave_max(best);
-        if (top == ninf) break;
-        const int id = wave_min(best == top ? lane + 64 * bi : 1 << 30);
-        const double sv = __shfl(bs, id & 63, 64);
-        total += sv;
-        my_id = lane == j ? id : my_id;
-        my_s = lane == j ? sv : my_s;
-#pragma unroll
-        for (int i = 0; i < EPL; i++) c[i] = lane + 64 * i == id ? ninf : c[i];
     }
-    if (lane < p.k) {
-        double w = my_s;
-        if (p.renorm && total != 0.0) w = w / total;
-        p.ids[(size_t)t * p.k + lane] = my_id;
-        p.weights[(size_t)t * p.k + lane] = (float)(w * (double)p.scale);
-        if (p.counts && my_id >= 0) atomicAdd(p.counts + my_id, 1);
+    int n = 0;
+#pragma unroll
+    for (int i = 0; i < EPL; i++) {
+        const bool in = a[i] >= t && a[i] != ninf;
+        const uint64_t mask = __builtin_amdgcn_ballot_w64(in);
+        const int at = n + below(mask);
+        if (in && at < 64) w.cand[at] = make_float2(l[i], __int_as_float(lane + 64 * i));
+        n += __builtin_popcountll(mask);
+    }
+    if (slow || n > 64) return whole<SOFT, L>(p, row, lds.v, m, sum);
+    // (one wave: its LDS accesses are performed in issue order)
+    __builtin_amdgcn_wave_barrier();
+    // candidate `lane` (in ascending id), its score and selection value
+    const float2 mine = w.cand[lane];
+    const bool there = lane < n;
+    const int id = there ? __float_as_int(mine.y) : 0;
+    const double s = score_of<SOFT>(there ? mine.x : 0.0f, m, sum);
+    double c = s + (p.bias ? (double)p.bias[id] : 0.0);
+    c = there ? (c != c ? (double)INFINITY : c) : -(double)INFINITY;
+    w.c[lane] = c;
+    __builtin_amdgcn_wave_barrier();
+    int rank = 0;
+    for (int j = 0; j < n; j += 2) {  // (past n: -inf, which no candidate's value is below)
+        const double o0 = w.c[j], o1 = w.c[min(j + 1, 63)];
+        rank += o0 > c || (o0 == c && j < lane) ? 1 : 0;
+        if (j + 1 < n) rank += o1 > c || (o1 == c && j + 1 < lane) ? 1 : 0;
+    }
+    if (there) {  // (distinct ranks 0 .. n - 1)
+        w.s[rank] = s;
+        w.id[rank] = id;
+    }
+    __builtin_amdgcn_wave_barrier();
+    Pick out = {-1, 0.0};
+    if (lane < min(n, p.k)) out = {w.id[lane], w.s[lane]};
+    __builtin_amdgcn_wave_barrier();
+    return out;
+}
+
+// Tokens of a block's waves in turn.  ALONE: the one block counts the choices
+// in LDS and writes the counts; else it clears them for k_gate_count.
+template <int EPL, bool SOFT, typename L, bool ALONE>
+__global__ __launch_bounds__(kGateWaves * 64) void k_gate(GateParams p)
+{
+    __shared__ GateLds<EPL> lds[kGateWaves];
+    __shared__ int hist[ALONE ? 64 * EPL : 1];
+    const int lane = threadIdx.x & 63, wv = threadIdx.x >> 6;
+    if (ALONE) {
+        for (int e = threadIdx.x; e < p.E; e += kGateWaves * 64) hist[e] = 0;
+        __syncthreads();
+    } else if (p.counts && blockIdx.x == 0) {
+        for (int e = threadIdx.x; e < p.E; e += kGateWaves * 64) p.counts[e] = 0;
+    }
+    float bias[EPL];
+#pragma unroll
+    for (int i = 0; i < EPL; i++) {
+        const int e = lane + 64 * i;
+        bias[i] = e < p.E ? (p.bias ? p.bias[e] : 0.0f) : -INFINITY;
+    }
+    const L *logits = reinterpret_cast<const L *>(p.logits);
+    for (int t = blockIdx.x * kGateWaves + wv; t < p.T; t += gridDim.x * kGateWaves) {
+        const L *row = logits + (size_t)t * p.ld;
+        float l[EPL];
+#pragma unroll
+        for (int i = 0; i < EPL; i++) l[i] = logit_f32<L>(row[min(lane + 64 * i, p.E - 1)]);
+        const Pick c = choose<EPL, SOFT, L>(p, row, l, bias, lds[wv]);
+        double w = c.s;
+        if (p.renorm) {
+            const double total = wave_sum64(lane < p.k ? c.s : 0.0);
+            w = total != 0.0 ? w / total : w;
+        }
+        if (lane < p.k) {
+            p.ids[(size_t)t * p.k + lane] = c.id;
+            p.weights[(size_t)t * p.k + lane] = (float)(w * (double)p.scale);
+            if (ALONE && c.id >= 0) atomicAdd(&hist[c.id], 1);
+        }
+    }
+    if (ALONE) {
+        __syncthreads();
+        for (int e = threadIdx.x; e < p.E; e += kGateWaves * 64) p.counts[e] = hist[e];
     }
 }
 
-__global__ __launch_bounds__(256) void k_gate_zero(int E, int32_t *counts)
+// the choices counted: a part of them per block in LDS, then one addition per
+// block and expert (one block alone writes its counts)
+__global__ __launch_bounds__(1024) void k_gate_count(GateParams p)
 {
-    const int e = blockIdx.x * 256 + threadIdx.x;
-    if (e < E) counts[e] = 0;
+    __shared__ int hist[kMaxExperts];
+    for (int e = threadIdx.x; e < p.E; e += 1024) hist[e] = 0;
+    __syncthreads();
+    const int64_t n = (int64_t)p.T * p.k;
+    for (int64_t i = (int64_t)blockIdx.x * 1024 + threadIdx.x; i < n; i += (int64_t)gridDim.x * 1024) {
+        const int id = p.ids[i];
+        if (id >= 0) atomicAdd(&hist[id], 1);
+    }
+    __syncthreads();
+    for (int e = threadIdx.x; e < p.E; e += 1024) {
+        if (gridDim.x == 1) p.counts[e] = hist[e];
+        else if (hist[e]) atomicAdd(p.counts + e, hist[e]);
+    }
+}
+
+constexpr int kGateBlocks = 1024;  // blocks at most; more tokens take turns
+constexpr int kCountPart = 8192;   // choices that a counting block takes
+
+template <int EPL, bool SOFT, typename L>
+void launch_epl(const GateParams &p, hipStream_t st)
+{
+    // (a token to each wave of one block: the counts in the same launch)
+    if (p.T <= kGateWaves && p.counts) {
+        k_gate<EPL, SOFT, L, true><<<1, kGateWaves * 64, 0, st>>>(p);
+        return;
+    }
+    const int blocks = (p.T + kGateWaves - 1) / kGateWaves;
+    k_gate<EPL, SOFT, L, false><<<blocks < kGateBlocks ? blocks : kGateBlocks, kGateWaves * 64, 0, st>>>(p);
+    if (p.counts) {
+        const int64_t parts = ((int64_t)p.T * p.k + kCountPart - 1) / kCountPart;
+        k_gate_count<<<(int)(parts < 64 ? parts : 64), 1024, 0, st>>>(p);
+    }
+}
+
+template <bool SOFT, typename L>
+void launch_score(const GateParams &p, hipStream_t st)
+{
+    const int epl = (p.E + 63) / 64;
+    if (epl <= 1) launch_epl<1, SOFT, L>(p, st);
+    else if (epl <= 2) launch_epl<2, SOFT, L>(p, st);
+    else if (epl <= 4) launch_epl<4, SOFT, L>(p, st);
+    else if (epl <= 8) launch_epl<8, SOFT, L>(p, st);
+    else if (epl <= 14) launch_epl<14, SOFT, L>(p, st);
+    else launch_epl<16, SOFT, L>(p, st);
 }
 
 template <typename L>
 void launch_typed(const GateParams &p, hipStream_t st)
 {
-    const int epl = (p.E + 63) / 64, grid = (p.T + 3) / 4;
-    if (epl <= 1) k_gate<1, L><<<grid, 256, 0, st>>>(p);
-    else if (epl <= 2) k_gate<2, L><<<grid, 256, 0, st>>>(p);
-    else if (epl <= 4) k_gate<4, L><<<grid, 256, 0, st>>>(p);
-    else if (epl <= 8) k_gate<8, L><<<grid, 256, 0, st>>>(p);
-    else k_gate<16, L><<<grid, 256, 0, st>>>(p);
+    if (p.softmax) launch_score<true, L>(p, st);
+    else launch_score<false, L>(p, st);
 }
 
 }  // namespace
 
 hipError_t launch_gate(const GateParams &p, int logits_type, hipStream_t st)
 {
-    if (p.counts) k_gate_zero<<<(p.E + 255) / 256, 256, 0, st>>>(p.E, p.counts);
     if (logits_type == 2) launch_typed<float>(p, st);
     else if (logits_type == 1) launch_typed<_Float16>(p, st);
     else launch_typed<uint16_t>(p, st);
