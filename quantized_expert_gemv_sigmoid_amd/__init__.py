@@ -346,19 +346,29 @@ def make_latent_desc(n_experts: int, top_k: int, hidden: int, latent: int, d_ffn
 
 # -------------------------------------------- routing from logits, dense product
 
-_types = None
+_torch = None  # torch, and what a call looks up in it
+_types = {}    # dtype -> moe_type
+_raw_stream = None
+
+
+def _setup() -> None:
+    global _torch, _raw_stream
+    import torch
+    _types.update({torch.bfloat16: BF16, torch.float16: F16, torch.float32: F32})
+    # (the current stream's address without a Stream object around it, where torch has it)
+    _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+        lambda i: torch.cuda.current_stream(i).cuda_stream)
+    _torch = torch
 
 
 def _type_of(t) -> int:
     """moe_type of a tensor's dtype."""
-    global _types
-    if _types is None:
-        import torch
-        _types = {torch.bfloat16: BF16, torch.float16: F16, torch.float32: F32}
-    try:
-        return _types[t.dtype]
-    except KeyError:
-        raise MoeError(EINVAL, f"dtype {t.dtype}") from None
+    if _torch is None:
+        _setup()
+    r = _types.get(t.dtype)
+    if r is None:
+        raise MoeError(EINVAL, f"dtype {t.dtype}")
+    return r
 
 
 def _rows(t, rows: int, cols: int, what: str) -> int:
@@ -366,32 +376,35 @@ def _rows(t, rows: int, cols: int, what: str) -> int:
     shape, stride = t.shape, t.stride()
     if len(shape) != 2 or shape[0] < rows or shape[1] != cols or (stride[1] != 1 and cols > 1):
         raise MoeError(EINVAL, f"{what}: {rows} rows of {cols} contiguous values wanted, got {tuple(shape)}, strides {tuple(stride)}")
-    return stride[0] if rows > 1 else max(stride[0], cols)
+    return stride[0] if rows > 1 or stride[0] > cols else cols
+
+
+def _flat(t, n: int, dtype, what: str):
+    """The address of n contiguous values of that dtype, or None."""
+    if t is None:
+        return None
+    if t.dtype != dtype or t.numel() < n or not t.is_contiguous():
+        raise MoeError(EINVAL, f"{what}: {n} contiguous {dtype} values wanted, got {tuple(t.shape)} {t.dtype}")
+    return t.data_ptr()
 
 
 def _same_device(first, *others) -> None:
+    d = first.device
     for t in others:
-        if t is not None and t.device != first.device:
-            raise MoeError(EINVAL, f"tensors on {first.device} and {t.device}")
+        if t is not None and t.device != d:
+            raise MoeError(EINVAL, f"tensors on {d} and {t.device}")
 
 
 def _call(x, stream, f, *args) -> int:
     """f(*args, stream) on x's device: that device's current stream where none is given."""
-    import torch
     i = x.device.index
-    if i != torch.cuda.current_device():
-        with torch.cuda.device(i):
-            return f(*args, _stream(stream))
-    return f(*args, _stream(stream))
-
-
-def _flat(t, n: int, dtype: str, what: str):
-    """The address of n contiguous values of that dtype, or None."""
-    if t is None:
-        return None
-    if t.numel() < n or not t.is_contiguous() or str(t.dtype) != dtype:
-        raise MoeError(EINVAL, f"{what}: {n} contiguous {dtype} values wanted, got {tuple(t.shape)} {t.dtype}")
-    return t.data_ptr()
+    if i is None:  # (not a GPU's: the arguments that were refused first aside, there is nothing to launch on)
+        raise MoeError(EINVAL, f"tensors on {x.device}")
+    s = _raw_stream(i) if stream is None else _stream(stream)
+    if i != _torch.cuda.current_device():
+        with _torch.cuda.device(i):
+            return f(*args, s)
+    return f(*args, s)
 
 
 def make_gate_desc(n_experts: int, top_k: int, score: int = SCORE_SIGMOID, bias=None,
@@ -403,7 +416,9 @@ def make_gate_desc(n_experts: int, top_k: int, score: int = SCORE_SIGMOID, bias=
     d.n_experts, d.top_k, d.score = n_experts, top_k, score
     d.n_groups, d.top_groups, d.group_score = n_groups, top_groups, group_score
     d.renorm, d.routed_scale = renorm, routed_scale
-    d.bias = _flat(bias, n_experts, "torch.float32", "bias")
+    if bias is not None and _type_of(bias) != F32:
+        raise MoeError(EINVAL, f"bias: {bias.dtype}")
+    d.bias = None if bias is None else _flat(bias, n_experts, bias.dtype, "bias")
     return d
 
 
@@ -411,10 +426,11 @@ def gate(desc: GateDesc, logits, T: int, ids, weights, counts=None, stream=None)
     """moe_gate on the first T rows of logits ([.., n_experts], float32, bfloat16 or float16;
     rows may be apart)."""
     E, n = desc.n_experts, T * desc.top_k
+    ty = _type_of(logits)
     _same_device(logits, ids, weights, counts)
-    _check(_call(logits, stream, lib().moe_gate, ctypes.byref(desc), logits.data_ptr(), _type_of(logits),
-                 _rows(logits, T, E, "logits"), T, _flat(ids, n, "torch.int32", "ids"),
-                 _flat(weights, n, "torch.float32", "weights"), _flat(counts, E, "torch.int32", "counts")),
+    i32 = _torch.int32
+    _check(_call(logits, stream, lib().moe_gate, desc, logits.data_ptr(), ty, _rows(logits, T, E, "logits"), T,
+                 _flat(ids, n, i32, "ids"), _flat(weights, n, _torch.float32, "weights"), _flat(counts, E, i32, "counts")),
            "moe_gate")
 
 
@@ -445,8 +461,8 @@ def make_linear_desc(w, w_up=None, bias=None, bias_up=None, act: int = LINEAR_NO
     d.bias_type = d.type if b is None else _type_of(b)
     d.residual_type = d.type if residual_type is None else residual_type
     d.w, d.w_up = w.data_ptr(), None if w_up is None else w_up.data_ptr()
-    d.bias = _flat(bias, n, str(b.dtype) if b is not None else "", "bias")
-    d.bias_up = _flat(bias_up, n, str(b.dtype) if b is not None else "", "bias_up")
+    d.bias = None if bias is None else _flat(bias, n, b.dtype, "bias")
+    d.bias_up = None if bias_up is None else _flat(bias_up, n, b.dtype, "bias_up")
     return d
 
 
@@ -488,5 +504,5 @@ def linear(desc: LinearDesc, x, T: int, out_half, out_f32, out_mode: int, ws, re
             raise MoeError(EINVAL, f"residual: {residual.dtype}")
         ldr, rp = _rows(residual, T, n, "residual"), residual.data_ptr()
     wp, wn = _ws(ws)
-    _check(_call(x, stream, lib().moe_linear, ctypes.byref(desc), x.data_ptr(), _rows(x, T, desc.n_in, "x"), T,
+    _check(_call(x, stream, lib().moe_linear, desc, x.data_ptr(), _rows(x, T, desc.n_in, "x"), T,
                  rp, ldr or 0, op, fp, n if ldo is None else ldo, out_mode, wp, wn), "moe_linear")

@@ -131,10 +131,10 @@ __device__ __forceinline__ int group_of(const GateParams &p, int e) { return (in
 // LDS of a wave: every expert's value (in `choose` the groups' part, as
 // floats; in `whole`), or the candidates
 struct GateCands {
-    float2 cand[64];  // logit, id
-    double c[64];     // selection values
-    double s[64];     // scores and ids by rank
     int id[64];
+    double c[64];  // selection values
+    double s[64];  // scores and ids by rank
+    int by[64];
 };
 template <int EPL>
 union GateLds {
@@ -200,6 +200,7 @@ __device__ __forceinline__ Pick whole(const GateParams &p, const L *row, double 
     for (int j = 0; j < p.k; j++) {
         if (look) {
             best = ninf;
+#pragma unroll 1
             for (int e = lane; e < p.E; e += 64) {
                 const double x = v[e];
                 const bool more = x > best && (p.groups == 1 || ((kept >> group_of(p, e)) & 1));  // (strict: the lower id of a tie)
@@ -230,47 +231,76 @@ __device__ __forceinline__ float margin(bool by_logit, float t)
     return by_logit ? 4.8e-7f * fabsf(t) + 1e-9f : 4.8e-7f + 2.4e-7f * fabsf(t);
 }
 
-// The choices of one token from its logits l (a copy of row's, lane l's
-// experts l + 64 i) and their biases (-inf: no expert, or one switched off;
-// 0 without a bias).
-template <int EPL, bool SOFT, typename L>
-__device__ __forceinline__ Pick choose(const GateParams &p, const L *row, const float (&l)[EPL], const float (&bias)[EPL],
-                                       GateLds<EPL> &lds)
+// the logits of a row that lane l holds: experts l, l + 64, ... (past the
+// end: the last one's), at `off` bytes
+template <int EPL, typename L>
+__device__ __forceinline__ void load_row(const L *row, const uint32_t (&off)[EPL], float (&l)[EPL])
 {
-    const int lane = threadIdx.x & 63;
+#pragma unroll
+    for (int i = 0; i < EPL; i++)
+        l[i] = logit_f32<L>(*reinterpret_cast<const L *>(reinterpret_cast<const char *>(row) + off[i]));
+}
+
+// the same lane number, but not known to be: what follows from it is computed
+// where it is used instead of being kept in registers over the token loop
+__device__ __forceinline__ int lane_here()
+{
+    int lane = threadIdx.x & 63;
+    asm volatile("" : "+v"(lane));
+    return lane;
+}
+
+// The choices of one token from its logits l and their biases (-inf: no
+// expert, or one switched off; 0 without a bias).  l is free, and filled with
+// the logits of the row `next`, once the experts' values are known.
+template <int EPL, bool SOFT, bool by_logit, typename L>
+__device__ __forceinline__ Pick choose(const GateParams &p, const L *row, const L *next, const uint32_t (&off)[EPL],
+                                       float (&l)[EPL], const float (&bias)[EPL], GateLds<EPL> &lds)
+{
+    const int lane = lane_here();
     const float ninf = -INFINITY;
-    const bool by_logit = !p.bias && !(p.groups > 1 && p.top2);
     GateCands &w = lds.n;
     float a[EPL];
     float m = ninf;
     double sum = 1.0;
-#pragma unroll
-    for (int i = 0; i < EPL; i++) a[i] = l[i] != ninf ? bias[i] : ninf;  // (-inf: takes no part)
     if (SOFT) {
 #pragma unroll
-        for (int i = 0; i < EPL; i++) m = fmaxf(m, a[i] != ninf ? l[i] : ninf);
+        for (int i = 0; i < EPL; i++) m = fmaxf(m, bias[i] != ninf ? l[i] : ninf);
         m = wave_max(m);
-        sum = 0.0;
+        if (!by_logit || !p.renorm) {  // (renormalised weights do not need it)
+            sum = 0.0;
 #pragma unroll
-        for (int i = 0; i < EPL; i++) {
-            sum += a[i] != ninf ? exp64(l[i] == m ? 0.0 : (double)l[i] - (double)m) : 0.0;
-            __builtin_amdgcn_sched_barrier(0);  // (one after the other: few registers)
+            for (int i = 0; i < EPL; i++) {
+                const double e = exp64(l[i] == m ? 0.0 : (double)l[i] - (double)m);
+                sum += l[i] != ninf && bias[i] != ninf ? e : 0.0;
+                __builtin_amdgcn_sched_barrier(0);  // (one after the other: few registers)
+            }
+            sum = wave_sum64(sum);
         }
-        sum = wave_sum64(sum);
-        if (!by_logit) {
-            const float inv = (float)(1.0 / sum);
-#pragma unroll
-            for (int i = 0; i < EPL; i++) a[i] = a[i] != ninf ? exp_hw(l[i] == m ? 0.0f : l[i] - m) * inv + a[i] : ninf;
-        }
-    } else if (!by_logit) {
-#pragma unroll
-        for (int i = 0; i < EPL; i++) a[i] = a[i] != ninf ? sigmoid_hw(l[i]) + a[i] : ninf;
     }
+    const float inv = (float)(1.0 / sum);
+    bool nan = false;
 #pragma unroll
     for (int i = 0; i < EPL; i++) {
-        const float v = by_logit ? (a[i] != ninf ? l[i] : ninf) : a[i];
-        a[i] = v != v ? (float)INFINITY : v;
+        float v = l[i];
+        if (!by_logit) v = SOFT ? exp_hw(v == m ? 0.0f : v - m) * inv : sigmoid_hw(v);
+        a[i] = l[i] != ninf ? v + bias[i] : ninf;  // (-inf: takes no part; without a bias + 0)
+        nan |= a[i] != a[i];
     }
+    if (__builtin_amdgcn_ballot_w64(nan)) {
+        bool hit = false;
+#pragma unroll
+        for (int i = 0; i < EPL; i++) {
+            a[i] = a[i] != a[i] ? (bias[i] != ninf ? (float)INFINITY : ninf) : a[i];
+            hit |= l[i] != l[i] && bias[i] != ninf;
+        }
+        if (SOFT && by_logit && __builtin_amdgcn_ballot_w64(hit)) {  // every score is NaN
+            sum = NAN;
+#pragma unroll
+            for (int i = 0; i < EPL; i++) a[i] = a[i] != ninf ? (float)INFINITY : ninf;
+        }
+    }
+    load_row<EPL, L>(next, off, l);
     // logits between which every two have different scores as doubles (the
     // sigmoid's reach 1, and both scores 0, further out)
     const float high = !by_logit || SOFT ? (float)INFINITY : 20.0f;
@@ -294,9 +324,10 @@ __device__ __forceinline__ Pick choose(const GateParams &p, const L *row, const 
         __builtin_amdgcn_wave_barrier();
     }
 
-    // t: a value that at least k lanes' maxima reach (or -inf), by halving
-    // the range of those maxima
-    float t = ninf;
+    // t: a value that at least k lanes' maxima reach (or the lowest one), by
+    // halving the range of those maxima
+    const float lowest = -3.4028234e38f;
+    float t = lowest;
     if (EPL > 1) {
         float top = ninf;
 #pragma unroll
@@ -304,6 +335,7 @@ __device__ __forceinline__ Pick choose(const GateParams &p, const L *row, const 
         float hi = wave_max(top), lo = -wave_max(top == ninf ? ninf : -top);
         if (__builtin_popcountll(__builtin_amdgcn_ballot_w64(top != ninf)) >= p.k) {
             t = lo;
+#pragma unroll 1
             for (int i = 0; i < 12; i++) {
                 const float mid = 0.5f * lo + 0.5f * hi;
                 const int n = __builtin_popcountll(__builtin_amdgcn_ballot_w64(top >= mid));
@@ -313,55 +345,60 @@ __device__ __forceinline__ Pick choose(const GateParams &p, const L *row, const 
             }
             t = fminf(t, high);
             if (t < INFINITY) t -= 2.0f * margin(by_logit, t);
-            if (t < low) t = ninf;
+            t = t < low ? lowest : fmaxf(t, lowest);
         }
     }
-    int n = 0;
+    // the lane's candidates as a set of its slots (the first slot the highest
+    // bit), then one of each lane's at a time into the list
+    uint32_t set = 0;
 #pragma unroll
-    for (int i = 0; i < EPL; i++) {
-        const bool in = a[i] >= t && a[i] != ninf;
-        const uint64_t mask = __builtin_amdgcn_ballot_w64(in);
-        const int at = n + below(mask);
-        if (in && at < 64) w.cand[at] = make_float2(l[i], __int_as_float(lane + 64 * i));
+    for (int i = 0; i < EPL; i++) set = set + set + (a[i] >= t ? 1u : 0u);
+    int n = 0;
+#pragma unroll 1
+    for (uint64_t mask; (mask = __builtin_amdgcn_ballot_w64(set != 0)) != 0;) {
+        const int top = 31 - __builtin_clz(set | 1u), at = n + below(mask);
+        if (set && at < 64) w.id[at] = lane + 64 * (EPL - 1 - top);
+        set &= ~(1u << top);
         n += __builtin_popcountll(mask);
     }
     if (slow || n > 64) return whole<SOFT, L>(p, row, lds.v, m, sum);
     // (one wave: its LDS accesses are performed in issue order)
     __builtin_amdgcn_wave_barrier();
-    // candidate `lane` (in ascending id), its score and selection value
-    const float2 mine = w.cand[lane];
+    // candidate `lane`, its score and selection value
     const bool there = lane < n;
-    const int id = there ? __float_as_int(mine.y) : 0;
-    const double s = score_of<SOFT>(there ? mine.x : 0.0f, m, sum);
+    const int id = there ? w.id[lane] : 0;
+    const double s = score_of<SOFT>(logit_f32<L>(row[id]), m, sum);
     double c = s + (p.bias ? (double)p.bias[id] : 0.0);
     c = there ? (c != c ? (double)INFINITY : c) : -(double)INFINITY;
     w.c[lane] = c;
     __builtin_amdgcn_wave_barrier();
     int rank = 0;
-    for (int j = 0; j < n; j += 2) {  // (past n: -inf, which no candidate's value is below)
-        const double o0 = w.c[j], o1 = w.c[min(j + 1, 63)];
-        rank += o0 > c || (o0 == c && j < lane) ? 1 : 0;
-        if (j + 1 < n) rank += o1 > c || (o1 == c && j + 1 < lane) ? 1 : 0;
+#pragma unroll 4
+    for (int j = 0; j < n; j++) rank += w.c[j] > c ? 1 : 0;
+    // (distinct values have the ranks 0 .. n - 1, equal ones share the least of theirs)
+    if (wave_sum(there ? (float)rank : 0.0f) != (float)(n * (n - 1) / 2)) {
+#pragma unroll 1
+        for (int j = 0; j < n; j++) rank += w.c[j] == c && w.id[j] < id ? 1 : 0;
     }
     if (there) {  // (distinct ranks 0 .. n - 1)
         w.s[rank] = s;
-        w.id[rank] = id;
+        w.by[rank] = id;
     }
     __builtin_amdgcn_wave_barrier();
     Pick out = {-1, 0.0};
-    if (lane < min(n, p.k)) out = {w.id[lane], w.s[lane]};
+    if (lane < min(n, p.k)) out = {w.by[lane], w.s[lane]};
     __builtin_amdgcn_wave_barrier();
     return out;
 }
 
 // Tokens of a block's waves in turn.  ALONE: the one block counts the choices
 // in LDS and writes the counts; else it clears them for k_gate_count.
-template <int EPL, bool SOFT, typename L, bool ALONE>
-__global__ __launch_bounds__(kGateWaves * 64) void k_gate(GateParams p)
+template <int EPL, bool SOFT, bool BY_LOGIT, typename L, bool ALONE>
+__global__ __launch_bounds__(kGateWaves * 64) __attribute__((amdgpu_waves_per_eu(4))) void k_gate(GateParams p)
 {
     __shared__ GateLds<EPL> lds[kGateWaves];
     __shared__ int hist[ALONE ? 64 * EPL : 1];
-    const int lane = threadIdx.x & 63, wv = threadIdx.x >> 6;
+    const int lane = threadIdx.x & 63, wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);  // (tokens in scalars)
     if (ALONE) {
         for (int e = threadIdx.x; e < p.E; e += kGateWaves * 64) hist[e] = 0;
         __syncthreads();
@@ -375,12 +412,16 @@ __global__ __launch_bounds__(kGateWaves * 64) void k_gate(GateParams p)
         bias[i] = e < p.E ? (p.bias ? p.bias[e] : 0.0f) : -INFINITY;
     }
     const L *logits = reinterpret_cast<const L *>(p.logits);
-    for (int t = blockIdx.x * kGateWaves + wv; t < p.T; t += gridDim.x * kGateWaves) {
-        const L *row = logits + (size_t)t * p.ld;
-        float l[EPL];
+    float l[EPL];
+    uint32_t off[EPL];
 #pragma unroll
-        for (int i = 0; i < EPL; i++) l[i] = logit_f32<L>(row[min(lane + 64 * i, p.E - 1)]);
-        const Pick c = choose<EPL, SOFT, L>(p, row, l, bias, lds[wv]);
+    for (int i = 0; i < EPL; i++) off[i] = (uint32_t)min(lane + 64 * i, p.E - 1) * (uint32_t)sizeof(L);
+    int t = blockIdx.x * kGateWaves + wv;
+    load_row<EPL, L>(logits + (size_t)min(t, p.T - 1) * p.ld, off, l);
+    for (; t < p.T; t += gridDim.x * kGateWaves) {
+        const L *row = logits + (size_t)t * p.ld;
+        const L *next = logits + (size_t)min(t + (int)gridDim.x * kGateWaves, p.T - 1) * p.ld;
+        const Pick c = choose<EPL, SOFT, BY_LOGIT, L>(p, row, next, off, l, bias, lds[wv]);
         double w = c.s;
         if (p.renorm) {
             const double total = wave_sum64(lane < p.k ? c.s : 0.0);
@@ -405,10 +446,14 @@ __global__ __launch_bounds__(1024) void k_gate_count(GateParams p)
     __shared__ int hist[kMaxExperts];
     for (int e = threadIdx.x; e < p.E; e += 1024) hist[e] = 0;
     __syncthreads();
-    const int64_t n = (int64_t)p.T * p.k;
-    for (int64_t i = (int64_t)blockIdx.x * 1024 + threadIdx.x; i < n; i += (int64_t)gridDim.x * 1024) {
-        const int id = p.ids[i];
-        if (id >= 0) atomicAdd(&hist[id], 1);
+    const int64_t n = (int64_t)p.T * p.k, step = (int64_t)gridDim.x * 1024;
+    for (int64_t i = (int64_t)blockIdx.x * 1024 + threadIdx.x; i < n; i += 4 * step) {
+        int id[4];
+#pragma unroll
+        for (int j = 0; j < 4; j++) id[j] = i + j * step < n ? p.ids[i + j * step] : -1;
+#pragma unroll
+        for (int j = 0; j < 4; j++)
+            if (id[j] >= 0) atomicAdd(&hist[id[j]], 1);
     }
     __syncthreads();
     for (int e = threadIdx.x; e < p.E; e += 1024) {
@@ -418,41 +463,44 @@ __global__ __launch_bounds__(1024) void k_gate_count(GateParams p)
 }
 
 constexpr int kGateBlocks = 1024;  // blocks at most; more tokens take turns
-constexpr int kCountPart = 8192;   // choices that a counting block takes
+constexpr int kCountPart = 4096;   // choices that a counting block takes
 
-template <int EPL, bool SOFT, typename L>
+template <int EPL, bool SOFT, bool BY_LOGIT, typename L>
 void launch_epl(const GateParams &p, hipStream_t st)
 {
     // (a token to each wave of one block: the counts in the same launch)
     if (p.T <= kGateWaves && p.counts) {
-        k_gate<EPL, SOFT, L, true><<<1, kGateWaves * 64, 0, st>>>(p);
+        k_gate<EPL, SOFT, BY_LOGIT, L, true><<<1, kGateWaves * 64, 0, st>>>(p);
         return;
     }
     const int blocks = (p.T + kGateWaves - 1) / kGateWaves;
-    k_gate<EPL, SOFT, L, false><<<blocks < kGateBlocks ? blocks : kGateBlocks, kGateWaves * 64, 0, st>>>(p);
+    k_gate<EPL, SOFT, BY_LOGIT, L, false><<<blocks < kGateBlocks ? blocks : kGateBlocks, kGateWaves * 64, 0, st>>>(p);
     if (p.counts) {
         const int64_t parts = ((int64_t)p.T * p.k + kCountPart - 1) / kCountPart;
         k_gate_count<<<(int)(parts < 64 ? parts : 64), 1024, 0, st>>>(p);
     }
 }
 
-template <bool SOFT, typename L>
+template <bool SOFT, bool BY_LOGIT, typename L>
 void launch_score(const GateParams &p, hipStream_t st)
 {
     const int epl = (p.E + 63) / 64;
-    if (epl <= 1) launch_epl<1, SOFT, L>(p, st);
-    else if (epl <= 2) launch_epl<2, SOFT, L>(p, st);
-    else if (epl <= 4) launch_epl<4, SOFT, L>(p, st);
-    else if (epl <= 8) launch_epl<8, SOFT, L>(p, st);
-    else if (epl <= 14) launch_epl<14, SOFT, L>(p, st);
-    else launch_epl<16, SOFT, L>(p, st);
+    if (epl <= 1) launch_epl<1, SOFT, BY_LOGIT, L>(p, st);
+    else if (epl <= 2) launch_epl<2, SOFT, BY_LOGIT, L>(p, st);
+    else if (epl <= 4) launch_epl<4, SOFT, BY_LOGIT, L>(p, st);
+    else if (epl <= 8) launch_epl<8, SOFT, BY_LOGIT, L>(p, st);
+    else if (epl <= 14) launch_epl<14, SOFT, BY_LOGIT, L>(p, st);
+    else launch_epl<16, SOFT, BY_LOGIT, L>(p, st);
 }
 
 template <typename L>
 void launch_typed(const GateParams &p, hipStream_t st)
 {
-    if (p.softmax) launch_score<true, L>(p, st);
-    else launch_score<false, L>(p, st);
+    const bool by_logit = !p.bias && !(p.groups > 1 && p.top2);
+    if (p.softmax && by_logit) launch_score<true, true, L>(p, st);
+    else if (p.softmax) launch_score<true, false, L>(p, st);
+    else if (by_logit) launch_score<false, true, L>(p, st);
+    else launch_score<false, false, L>(p, st);
 }
 
 }  // namespace
