@@ -394,7 +394,17 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(1, 1))) voi
     for (; 64 * (s + 4) <= K; s += 2) two_stages(No{});
     for (; s < S; s += 2) two_stages(Yes{});
     __builtin_amdgcn_sched_barrier(0);
-    asm volatile("s_nop 15\n\ts_nop 15" ::: "memory");  // the last products' results (written-out products: the compiler does not wait)
+    // The last products' results: nobody else waits for written-out products,
+    // so every sum goes through a statement behind the wait.
+    asm volatile("s_nop 15\n\ts_nop 15" ::: "memory");
+#pragma unroll
+    for (int i = 0; i < 4; i++) {
+        f32x4_t(&c)[4][4] = acc[i >> 1][i & 1];
+        asm volatile(""
+                     : "+a"(c[0][0]), "+a"(c[0][1]), "+a"(c[0][2]), "+a"(c[0][3]), "+a"(c[1][0]), "+a"(c[1][1]), "+a"(c[1][2]),
+                       "+a"(c[1][3]), "+a"(c[2][0]), "+a"(c[2][1]), "+a"(c[2][2]), "+a"(c[2][3]), "+a"(c[3][0]), "+a"(c[3][1]),
+                       "+a"(c[3][2]), "+a"(c[3][3]));
+    }
     wait_copies<0>();
     barrier();
 

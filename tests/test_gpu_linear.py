@@ -147,6 +147,47 @@ def test_whole_numbers_are_exact(T, K, N, dtype):
     assert torch.equal(h, v.float().to(dtype))
 
 
+# sizes at which the rule takes each of its kernels, with and without a split of K: served batches of up to 8, 16 and 32
+# tokens a block, tiles of 64 x 32 to 256 x 256, and the tiles for rows that are not 16-byte aligned
+KERNELS = [(5, 1000, 700), (13, 1000, 5000), (70, 4104, 1000), (30, 2056, 3000), (40, 1000, 4000), (260, 4104, 500),
+           (100, 2056, 4000), (600, 4104, 512), (200, 2056, 4000), (1000, 8200, 260), (400, 1032, 4000), (200, 7176, 900),
+           (1000, 1032, 2500), (140, 7176, 7000), (1000, 1160, 4000), (2060, 520, 4104), (1030, 6152, 6000), (300, 1025, 2001),
+           (24, 4097, 300), (500, 1025, 2001), (60, 3585, 3587), (700, 2049, 1000), (1500, 1025, 2001)]
+KERNELS_GATED = [(5, 1000, 700), (13, 1000, 3000), (30, 2056, 1500), (100, 2056, 2000), (400, 1032, 2000), (520, 1032, 1800),
+                 (1000, 1160, 2000), (1000, 4104, 2052), (2060, 520, 2052), (500, 1025, 1001), (700, 2049, 500), (9, 4097, 150)]
+
+
+@pytest.mark.parametrize("T,K,N", KERNELS)
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
+def test_every_kernel_is_exact(T, K, N, dtype):
+    print(f"case: T={T} K={K} N={N} {dtype}", flush=True)
+    s = make(T, K, N, dtype, bias=torch.float32, residual=dtype, whole=True, seed=T + K + N)
+    v, _ = reference(s)
+    h, f = call(s, moe.OUT_BOTH)
+    assert torch.equal(f.double(), v)
+    assert torch.equal(h, v.float().to(dtype))
+
+
+@pytest.mark.parametrize("T,K,N", KERNELS_GATED)
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
+def test_every_gated_kernel(T, K, N, dtype):
+    print(f"case: T={T} K={K} N={N} {dtype}", flush=True)
+    s = make(T, K, N, dtype, act="swiglu", bias=dtype, residual=torch.float32, seed=T + K + N)
+    h, f = call(s, moe.OUT_BOTH)
+    check(s, f, torch.float32)
+    assert torch.equal(h, f.to(dtype))
+    # gates of 30 and more: sigmoid is 1 in fp32, so whole numbers make whole numbers
+    s = make(T, K, N, dtype, act="swiglu", whole=True, seed=T)
+    s["bias"] = torch.full((N,), 4096.0, device="cuda")
+    s["bias_up"] = torch.zeros(N, device="cuda")
+    s["x"].clamp_(-1, 1)
+    s["w"].mul_(0).add_(1)       # gate: 4096 + the sum of a row of -1 .. 1, above 4096 - 5 sqrt(K)
+    v, _ = reference(s)
+    keep = v.abs() < 2 ** 24     # (whole numbers that fp32 holds)
+    _, f = call(s, moe.OUT_F32)
+    assert torch.equal(f.double()[keep], v[keep].round())
+
+
 @pytest.mark.parametrize("T,K,N", SIZES)
 @pytest.mark.parametrize("act", GATED)
 def test_gated_sizes(T, K, N, act):
@@ -257,7 +298,8 @@ def test_no_overflow_between_fp16_and_output():
 
 
 @pytest.mark.parametrize("T,K,N,act", [(1, 1024, 512, "none"), (30, 1024, 512, "swiglu"), (200, 2048, 320, "silu"),
-                                       (700, 1536, 640, "situ_glu"), (64, 4096, 64, "none"), (90, 1117, 513, "gelu")])
+                                       (700, 1536, 640, "situ_glu"), (64, 4096, 64, "none"), (90, 1117, 513, "gelu"),
+                                       (2060, 520, 4104, "none"), (1030, 6152, 6000, "relu")])
 def test_captured_and_replayed(T, K, N, act):
     """Replays between eager work equal the eager call, two graphs in turn on one workspace among them."""
     print(f"case: T={T} K={K} N={N} {act}", flush=True)
