@@ -97,42 +97,52 @@ __device__ __forceinline__ uint2 pack4(float a, float b, float c, float d)
     return make_uint2(__builtin_bit_cast(uint32_t, x), __builtin_bit_cast(uint32_t, y));
 }
 
-// R rows of four outputs each, n .. n + 3 of tokens t[i], from their sums a
-// and u (biases included); rows with t[i] < 0 are not there.  p.vec: all four
-// outputs exist and every row of the residual and the outputs is aligned for
-// them.
-template <bool F16, bool GATED, int R>
-__device__ __forceinline__ void finish_rows(const LinearParams &p, const int (&t)[R], int n, float (&a)[4 * R],
-                                            const float (&u)[4 * R])
+// The residual's four values at n .. n + 3 of R tokens t[i] (none where
+// t[i] < 0), as they are in memory; with p.vec only.
+template <int R>
+__device__ __forceinline__ void load_res(const LinearParams &p, const int (&t)[R], int n, uint4 (&r)[R])
 {
-    activate<GATED>(a, u, p.act, p.b1, p.b2);
-    const float *rf = reinterpret_cast<const float *>(p.res);
-    const uint16_t *rh = reinterpret_cast<const uint16_t *>(p.res);
+    if (!p.res || !p.vec) return;
+    if (p.res_f32) {
+#pragma unroll
+        for (int i = 0; i < R; i++)
+            if (t[i] >= 0)
+                r[i] = *reinterpret_cast<const uint4 *>(reinterpret_cast<const float *>(p.res) + (size_t)t[i] * p.ldr + n);
+    } else {
+#pragma unroll
+        for (int i = 0; i < R; i++)
+            if (t[i] >= 0) {
+                const uint2 v = *reinterpret_cast<const uint2 *>(reinterpret_cast<const uint16_t *>(p.res) + (size_t)t[i] * p.ldr + n);
+                r[i].x = v.x;
+                r[i].y = v.y;
+            }
+    }
+}
+
+// R rows of four outputs each, n .. n + 3 of tokens t[i], from their
+// activated sums a and load_res's values; rows with t[i] < 0 are not there.
+// p.vec: all four outputs exist and every row of the residual and the outputs
+// is aligned for them.
+template <bool F16, int R>
+__device__ __forceinline__ void write_rows(const LinearParams &p, const int (&t)[R], int n, float (&a)[4 * R], const uint4 (&r)[R])
+{
     uint16_t *oh = reinterpret_cast<uint16_t *>(p.out_half);
     if (p.vec) {
         if (p.res && p.res_f32) {
-            float4 v[R];
-#pragma unroll
-            for (int i = 0; i < R; i++)
-                if (t[i] >= 0) v[i] = *reinterpret_cast<const float4 *>(rf + (size_t)t[i] * p.ldr + n);
 #pragma unroll
             for (int i = 0; i < R; i++) {
-                a[4 * i] += v[i].x;
-                a[4 * i + 1] += v[i].y;
-                a[4 * i + 2] += v[i].z;
-                a[4 * i + 3] += v[i].w;
+                a[4 * i] += __uint_as_float(r[i].x);
+                a[4 * i + 1] += __uint_as_float(r[i].y);
+                a[4 * i + 2] += __uint_as_float(r[i].z);
+                a[4 * i + 3] += __uint_as_float(r[i].w);
             }
         } else if (p.res) {
-            ushort4 v[R];
-#pragma unroll
-            for (int i = 0; i < R; i++)
-                if (t[i] >= 0) v[i] = *reinterpret_cast<const ushort4 *>(rh + (size_t)t[i] * p.ldr + n);
 #pragma unroll
             for (int i = 0; i < R; i++) {
-                a[4 * i] += half_f32<F16>(v[i].x);
-                a[4 * i + 1] += half_f32<F16>(v[i].y);
-                a[4 * i + 2] += half_f32<F16>(v[i].z);
-                a[4 * i + 3] += half_f32<F16>(v[i].w);
+                a[4 * i] += half_f32<F16>((uint16_t)r[i].x);
+                a[4 * i + 1] += half_f32<F16>((uint16_t)(r[i].x >> 16));
+                a[4 * i + 2] += half_f32<F16>((uint16_t)r[i].y);
+                a[4 * i + 3] += half_f32<F16>((uint16_t)(r[i].y >> 16));
             }
         }
         if (oh) {
@@ -151,6 +161,8 @@ __device__ __forceinline__ void finish_rows(const LinearParams &p, const int (&t
         }
         return;
     }
+    const float *rf = reinterpret_cast<const float *>(p.res);
+    const uint16_t *rh = reinterpret_cast<const uint16_t *>(p.res);
 #pragma unroll
     for (int i = 0; i < R; i++) {
         if (t[i] < 0) continue;
@@ -164,6 +176,17 @@ __device__ __forceinline__ void finish_rows(const LinearParams &p, const int (&t
             if (p.out_f32) p.out_f32[at + j] = v;
         }
     }
+}
+
+// one row of sums (biases included), its residual loaded here
+template <bool F16, bool GATED>
+__device__ __forceinline__ void finish_row(const LinearParams &p, int t, int n, float (&a)[4], const float (&u)[4])
+{
+    const int tt[1] = {t};
+    uint4 r[1] = {};
+    load_res<1>(p, tt, n, r);
+    activate<GATED>(a, u, p.act, p.b1, p.b2);
+    write_rows<F16, 1>(p, tt, n, a, r);
 }
 
 // the biases of outputs n .. n + 3
@@ -249,6 +272,15 @@ __device__ __forceinline__ __amdgpu_buffer_rsrc_t rows_rsrc(const uint16_t *base
 __device__ __forceinline__ void copy16(__amdgpu_buffer_rsrc_t r, uint32_t dst, uint32_t voff)
 {
     asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds"
+                 :
+                 : "s"(__builtin_amdgcn_readfirstlane(dst)), "v"(voff), "s"(r)
+                 : "memory", "m0");
+}
+
+// 4 bytes per lane, likewise
+__device__ __forceinline__ void copy4(__amdgpu_buffer_rsrc_t r, uint32_t dst, uint32_t voff)
+{
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dword %1, %2, 0 offen lds"
                  :
                  : "s"(__builtin_amdgcn_readfirstlane(dst)), "v"(voff), "s"(r)
                  : "memory", "m0");
@@ -388,10 +420,28 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(1, 1))) voi
         kc0 += 128;
         kc1 += 128;
     };
+    // The tile's residual on its way into the L2 while the last stages are
+    // multiplied: 4 bytes of every 128 of its rows, to an unused place.
+    auto warm_res = [&] {
+        if (!p.res || !p.vec || ksplit > 1) return;
+        const int sz = p.res_f32 ? 4 : 2, rows = min(256, p.M - t0), cols = min(GATED ? 128 : 256, p.N - n0);
+        const char *base = reinterpret_cast<const char *>(p.res) + ((size_t)t0 * p.ldr + n0) * sz;
+        const int lines = (cols * sz + 127) >> 7;  // of a row, up to 8
+#pragma unroll 1
+        for (int i = wv * 64; i < rows * lines; i += 256) {
+            const int e = i + lane, row = e / lines, line = e - row * lines;
+            // (rows in 64 bits: a resource of its own for each 64 lines' first row)
+            const int r0 = i / lines;
+            const __amdgpu_buffer_rsrc_t rr = grsrc(base + (size_t)r0 * p.ldr * sz, 0x7fffffffu);
+            const uint32_t off = (uint32_t)((row - r0) * p.ldr * sz) + line * 128;
+            copy4(rr, (uint32_t)(uintptr_t)lds + kBigRing + wv * 256, row < rows ? off & ~3u : 0x80000000u);
+        }
+    };
     // (the copies of stages up to s + 3 stay inside K while 64 (s + 4) <= K)
     const int S = (K + 63) / 64;
     int s = 0;
     for (; 64 * (s + 4) <= K; s += 2) two_stages(No{});
+    warm_res();
     for (; s < S; s += 2) two_stages(Yes{});
     __builtin_amdgcn_sched_barrier(0);
     // The last products' results: nobody else waits for written-out products,
@@ -414,9 +464,33 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(1, 1))) voi
     LDS uint8_t *buf = lds + wv * kBigWave;
     const int c4 = (lane & 15) * 4;
     const int row_l = r16 * kBigRow + q4 * 16;
-    constexpr int R = 4;
+    constexpr int ROWS = GATED ? 64 : 128, R = 4, BATCHES = ROWS / (4 * R);
 #pragma unroll 1
     for (int round = 0; round < 2; round++) {
+        const int n = n0 + (GATED ? 0 : round * 128) + wn * 64 + c4;
+        auto token = [&](int r) {
+            const int t = t0 + (GATED ? round * 128 + r : (r >> 6) * 128 + (r & 63)) + wt * 64;
+            return t < p.M && n < p.N ? t : -1;
+        };
+        auto sums = [&](int r) { return reinterpret_cast<LDS f32x4_t *>(buf + r * kBigRow + c4 * 4); };
+        // The residual of a whole tile goes to registers at once, before any
+        // store: a load waits for the stores before it to reach memory, so
+        // batches that load and store in turn took 22 us more per 256 tiles
+        // of fp16 residuals.  (Rows 4 k of the lane's, at scalar distances.)
+        const uint32_t rsz = p.res_f32 ? 4 : 2, rld = (uint32_t)p.ldr * rsz;
+        const __amdgpu_buffer_rsrc_t rr = grsrc(
+            reinterpret_cast<const char *>(p.res) +
+                ((size_t)(t0 + (GATED ? round * 128 : 0) + wt * 64) * p.ldr + n0 + (GATED ? 0 : round * 128) + wn * 64) * rsz,
+            0xfffffffcu);
+        const int rv = (int)(q4 * rld + c4 * rsz);
+        auto rowoff = [&](int k) { return (int)((uint32_t)((4 * k >> 6) * 128 + (4 * k & 63)) * rld); };
+        const bool direct = ksplit == 1 && p.res && p.vec && t0 + 256 <= p.M && n0 + (GATED ? 128 : 256) <= p.N;
+        uint2 early[ROWS / 4] = {};
+        if (direct && !p.res_f32) {
+#pragma unroll
+            for (int k = 0; k < ROWS / 4; k++)
+                early[k] = __builtin_bit_cast(uint2, __builtin_amdgcn_raw_buffer_load_b64(rr, rv, rowoff(k), 0));
+        }
         auto put = [&](int row, const f32x4_t(&c)[4][4]) {
 #pragma unroll
             for (int f = 0; f < 4; f++)
@@ -431,39 +505,88 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(1, 1))) voi
             put(0, GATED ? acc[0][1] : acc[1][0]);
             put(64, acc[1][1]);
         }
-        const int n = n0 + (GATED ? 0 : round * 128) + wn * 64 + c4;
-        if (n < p.N) {
-            float ba[4], bu[4] = {};
-            bias4<F16>(p.bias, p.bias_f32, n, p.N, ba);
-            if (GATED) bias4<F16>(p.bias_up, p.bias_f32, n, p.N, bu);
-            if (ksplit > 1) {
-                for (int r = q4; r < (GATED ? 64 : 128); r += 4) {
-                    const int t = t0 + (GATED ? round * 128 + r : (r >> 6) * 128 + (r & 63)) + wt * 64;
-                    if (t >= p.M) continue;
-                    store_part<GATED>(p, ks, t, n, *reinterpret_cast<const LDS f32x4_t *>(buf + r * kBigRow + c4 * 4),
-                                      *reinterpret_cast<const LDS f32x4_t *>(buf + ((GATED ? 64 : 0) + r) * kBigRow + c4 * 4));
+        if (ksplit > 1) {
+            for (int r = q4; r < ROWS; r += 4)
+                if (const int t = token(r); t >= 0) store_part<GATED>(p, ks, t, n, *sums(r), *sums((GATED ? 64 : 0) + r));
+            continue;
+        }
+        float ba[4], bu[4] = {};
+        bias4<F16>(p.bias, p.bias_f32, n, p.N, ba);
+        if (GATED) bias4<F16>(p.bias_up, p.bias_f32, n, p.N, bu);
+        auto activated = [&](int r0, float(&a)[4 * R]) {  // rows r0 + 4 i
+            float u[4 * R];
+#pragma unroll
+            for (int i = 0; i < R; i++) {
+                const f32x4_t c = *sums(r0 + 4 * i);
+                f32x4_t d = {};
+                if (GATED) d = *sums(64 + r0 + 4 * i);
+#pragma unroll
+                for (int j = 0; j < 4; j++) {
+                    a[4 * i + j] = c[j] + ba[j];
+                    u[4 * i + j] = GATED ? d[j] + bu[j] : 0.0f;
                 }
-                continue;
             }
+            activate<GATED>(a, u, p.act, p.b1, p.b2);
+        };
+        if (!direct) {
 #pragma unroll 1
-            for (int r0 = q4; r0 < (GATED ? 64 : 128); r0 += 4 * R) {
+            for (int r0 = q4; r0 < ROWS; r0 += 4 * R) {
                 int t[R];
-                float a[4 * R], u[4 * R];
+                float a[4 * R];
+                uint4 res[R] = {};
 #pragma unroll
-                for (int i = 0; i < R; i++) {
-                    const int r = r0 + 4 * i;
-                    t[i] = t0 + (GATED ? round * 128 + r : (r >> 6) * 128 + (r & 63)) + wt * 64;
-                    t[i] = t[i] < p.M ? t[i] : -1;
-                    const f32x4_t c = *reinterpret_cast<const LDS f32x4_t *>(buf + r * kBigRow + c4 * 4);
-                    f32x4_t d = {};
-                    if (GATED) d = *reinterpret_cast<const LDS f32x4_t *>(buf + (64 + r) * kBigRow + c4 * 4);
+                for (int i = 0; i < R; i++) t[i] = token(r0 + 4 * i);
+                load_res<R>(p, t, n, res);
+                activated(r0, a);
+                write_rows<F16, R>(p, t, n, a, res);
+            }
+            continue;
+        }
+        if (GATED || p.act != MOE_LINEAR_NONE || p.bias) {
+#pragma unroll 1
+            for (int r0 = q4; r0 < ROWS; r0 += 4 * R) {
+                float a[4 * R];
+                activated(r0, a);
 #pragma unroll
-                    for (int j = 0; j < 4; j++) {
-                        a[4 * i + j] = c[j] + ba[j];
-                        u[4 * i + j] = GATED ? d[j] + bu[j] : 0.0f;
-                    }
-                }
-                finish_rows<F16, GATED, R>(p, t, n, a, u);
+                for (int i = 0; i < R; i++) *sums(r0 + 4 * i) = f32x4_t{a[4 * i], a[4 * i + 1], a[4 * i + 2], a[4 * i + 3]};
+            }
+        }
+        auto batch = [&](int b, const uint4(&res)[R]) {
+            int t[R];
+            float a[4 * R];
+#pragma unroll
+            for (int i = 0; i < R; i++) {
+                const int r = q4 + 4 * (b * R + i);
+                t[i] = token(r);
+                const f32x4_t c = *sums(r);
+#pragma unroll
+                for (int j = 0; j < 4; j++) a[4 * i + j] = c[j];
+            }
+            write_rows<F16, R>(p, t, n, a, res);
+        };
+        if (!p.res_f32) {
+#pragma unroll
+            for (int b = 0; b < BATCHES; b++) {
+                uint4 res[R];
+#pragma unroll
+                for (int i = 0; i < R; i++) res[i] = make_uint4(early[b * R + i].x, early[b * R + i].y, 0, 0);
+                batch(b, res);
+                __builtin_amdgcn_sched_barrier(0);
+            }
+        } else {
+            constexpr int PART = BATCHES / 4;  // (fp32: a quarter of the rows at a time)
+#pragma unroll
+            for (int q = 0; q < 4; q++) {
+                uint4 res[PART][R];
+#pragma unroll
+                for (int b = 0; b < PART; b++)
+#pragma unroll
+                    for (int i = 0; i < R; i++)
+                        res[b][i] = __builtin_bit_cast(
+                            uint4, __builtin_amdgcn_raw_buffer_load_b128(rr, rv, rowoff((q * PART + b) * R + i), 0));
+#pragma unroll
+                for (int b = 0; b < PART; b++) batch(q * PART + b, res[b]);
+                __builtin_amdgcn_sched_barrier(0);
             }
         }
     }
@@ -706,7 +829,7 @@ __global__ __launch_bounds__(WN * WT * 64) void k_linear_tile(LinearParams p, in
                 a[j] = c[j] + ba[j];
                 u[j] = GATED ? d[j] + bu[j] : 0.0f;
             }
-            finish_rows<F16, GATED, 1>(p, t, n, a, u);
+            finish_row<F16, GATED>(p, t[0], n, a, u);
         }
     }
 }
@@ -738,7 +861,7 @@ __global__ __launch_bounds__(256) void k_linear_join(LinearParams p)
         a[j] = v[0][j] + ba[j];
         u[j] = GATED ? v[PL - 1][j] + bu[j] : 0.0f;
     }
-    finish_rows<F16, GATED, 1>(p, t, n, a, u);
+    finish_row<F16, GATED>(p, t[0], n, a, u);
 }
 
 // ------------------------------------------------------------ served batches
@@ -855,7 +978,7 @@ __global__ __launch_bounds__(kFewWaves * 64) void k_linear_few(LinearParams p)
             a[e] = ca[e] + ba[e];
             u[e] = cu[e] + bu[e];
         }
-        finish_rows<F16, GATED, 1>(p, t, n, a, u);
+        finish_row<F16, GATED>(p, t[0], n, a, u);
     }
 }
 
