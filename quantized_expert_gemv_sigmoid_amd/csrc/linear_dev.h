@@ -42,6 +42,29 @@ __device__ __forceinline__ uint16_t f32_half(float v)
     return F16 ? __builtin_bit_cast(uint16_t, (_Float16)v) : f32_to_bf16_rne(v);
 }
 
+// tanh(x) = n / d for x >= 0, e = exp(-2 x): (1 - e) / (1 + e), and below
+// 1/16, where 1 - e cancels, the odd Taylor polynomial to x^7 (the next term
+// is below 3e-13 of it)
+__device__ __forceinline__ void tanh_parts(float x, float e, float &n, float &d)
+{
+    const float x2 = x * x;
+    const float small = x * (1.0f + x2 * (-1.0f / 3.0f + x2 * (2.0f / 15.0f + x2 * (-17.0f / 315.0f))));
+    n = x < 0.0625f ? small : 1.0f - e;
+    d = x < 0.0625f ? 1.0f : 1.0f + e;
+}
+
+// SiTU-GLU b1 tanh(g / b1) sigmoid(g) b2 tanh(u / b2) with one reciprocal for
+// the three quotients (r1 = 1 / b1, r2 = 1 / b2, b12 = b1 b2)
+__device__ __forceinline__ float situ_glu(float g, float u, float r1, float r2, float b12)
+{
+    const float x = fabsf(g) * r1, y = fabsf(u) * r2;
+    float n1, d1, n2, d2;
+    tanh_parts(x, exp_hw(-2.0f * x), n1, d1);
+    tanh_parts(y, exp_hw(-2.0f * y), n2, d2);
+    const float h = (b12 * n1) * n2 * rcp_hw(d1 * d2 * (1.0f + exp_hw(-g)));
+    return __uint_as_float(__float_as_uint(h) ^ ((__float_as_uint(g) ^ __float_as_uint(u)) & 0x80000000u));
+}
+
 // a[i] = act(a[i], u[i]): one branch for all NV values
 template <bool GATED, int NV>
 __device__ __forceinline__ void activate(float (&a)[NV], const float (&u)[NV], int act, float b1, float b2)
@@ -49,7 +72,7 @@ __device__ __forceinline__ void activate(float (&a)[NV], const float (&u)[NV], i
     if (GATED) {
         if (act == MOE_LINEAR_SITU_GLU) {
 #pragma unroll
-            for (int i = 0; i < NV; i++) a[i] = gated_act(a[i], u[i], 0, b1, b2);
+            for (int i = 0; i < NV; i++) a[i] = situ_glu(a[i], u[i], 1.0f / b1, 1.0f / b2, b1 * b2);
         } else {
 #pragma unroll
             for (int i = 0; i < NV; i++) a[i] = gated_act(a[i], u[i], 1, b1, b2);
@@ -243,6 +266,8 @@ __device__ __forceinline__ void barrier()
     asm volatile("" ::: "memory");
 }
 
+typedef uint32_t u32x2_t __attribute__((ext_vector_type(2)));
+
 template <bool F16>
 struct Frag {
     using V = typename std::conditional<F16, f16x8_t, bf16x8_t>::type;
@@ -272,15 +297,6 @@ __device__ __forceinline__ __amdgpu_buffer_rsrc_t rows_rsrc(const uint16_t *base
 __device__ __forceinline__ void copy16(__amdgpu_buffer_rsrc_t r, uint32_t dst, uint32_t voff)
 {
     asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds"
-                 :
-                 : "s"(__builtin_amdgcn_readfirstlane(dst)), "v"(voff), "s"(r)
-                 : "memory", "m0");
-}
-
-// 4 bytes per lane, likewise
-__device__ __forceinline__ void copy4(__amdgpu_buffer_rsrc_t r, uint32_t dst, uint32_t voff)
-{
-    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dword %1, %2, 0 offen lds"
                  :
                  : "s"(__builtin_amdgcn_readfirstlane(dst)), "v"(voff), "s"(r)
                  : "memory", "m0");
@@ -420,28 +436,10 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(1, 1))) voi
         kc0 += 128;
         kc1 += 128;
     };
-    // The tile's residual on its way into the L2 while the last stages are
-    // multiplied: 4 bytes of every 128 of its rows, to an unused place.
-    auto warm_res = [&] {
-        if (!p.res || !p.vec || ksplit > 1) return;
-        const int sz = p.res_f32 ? 4 : 2, rows = min(256, p.M - t0), cols = min(GATED ? 128 : 256, p.N - n0);
-        const char *base = reinterpret_cast<const char *>(p.res) + ((size_t)t0 * p.ldr + n0) * sz;
-        const int lines = (cols * sz + 127) >> 7;  // of a row, up to 8
-#pragma unroll 1
-        for (int i = wv * 64; i < rows * lines; i += 256) {
-            const int e = i + lane, row = e / lines, line = e - row * lines;
-            // (rows in 64 bits: a resource of its own for each 64 lines' first row)
-            const int r0 = i / lines;
-            const __amdgpu_buffer_rsrc_t rr = grsrc(base + (size_t)r0 * p.ldr * sz, 0x7fffffffu);
-            const uint32_t off = (uint32_t)((row - r0) * p.ldr * sz) + line * 128;
-            copy4(rr, (uint32_t)(uintptr_t)lds + kBigRing + wv * 256, row < rows ? off & ~3u : 0x80000000u);
-        }
-    };
     // (the copies of stages up to s + 3 stay inside K while 64 (s + 4) <= K)
     const int S = (K + 63) / 64;
     int s = 0;
     for (; 64 * (s + 4) <= K; s += 2) two_stages(No{});
-    warm_res();
     for (; s < S; s += 2) two_stages(Yes{});
     __builtin_amdgcn_sched_barrier(0);
     // The last products' results: nobody else waits for written-out products,
@@ -473,23 +471,26 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(1, 1))) voi
             return t < p.M && n < p.N ? t : -1;
         };
         auto sums = [&](int r) { return reinterpret_cast<LDS f32x4_t *>(buf + r * kBigRow + c4 * 4); };
-        // The residual of a whole tile goes to registers at once, before any
-        // store: a load waits for the stores before it to reach memory, so
-        // batches that load and store in turn took 22 us more per 256 tiles
-        // of fp16 residuals.  (Rows 4 k of the lane's, at scalar distances.)
-        const uint32_t rsz = p.res_f32 ? 4 : 2, rld = (uint32_t)p.ldr * rsz;
-        const __amdgpu_buffer_rsrc_t rr = grsrc(
-            reinterpret_cast<const char *>(p.res) +
-                ((size_t)(t0 + (GATED ? round * 128 : 0) + wt * 64) * p.ldr + n0 + (GATED ? 0 : round * 128) + wn * 64) * rsz,
-            0xfffffffcu);
-        const int rv = (int)(q4 * rld + c4 * rsz);
-        auto rowoff = [&](int k) { return (int)((uint32_t)((4 * k >> 6) * 128 + (4 * k & 63)) * rld); };
-        const bool direct = ksplit == 1 && p.res && p.vec && t0 + 256 <= p.M && n0 + (GATED ? 128 : 256) <= p.N;
+        // Whole tiles with aligned rows: rows 4 k of the lane's at scalar
+        // distances from its first.  Their residual goes to registers at once,
+        // before any store: a load waits for the stores before it to reach
+        // memory, so batches that load and store in turn took 22 us more per
+        // 256 tiles of 16-bit residuals.
+        const bool direct = ksplit == 1 && p.vec && t0 + 256 <= p.M && n0 + (GATED ? 128 : 256) <= p.N;
+        const int tr = t0 + (GATED ? round * 128 : 0) + wt * 64, nr = n0 + (GATED ? 0 : round * 128) + wn * 64;
+        auto rows_of = [&](const void *base, int64_t ld, int sz) {
+            return grsrc(reinterpret_cast<const char *>(base) + ((size_t)tr * ld + nr) * sz, 0xfffffffcu);
+        };
+        auto row_at = [&](int k, int64_t ld, int sz) { return (int)((uint32_t)((4 * k >> 6) * 128 + (4 * k & 63)) * (uint32_t)(ld * sz)); };
+        auto lane_at = [&](int64_t ld, int sz) { return (int)(q4 * (uint32_t)(ld * sz) + c4 * sz); };
+        const __amdgpu_buffer_rsrc_t rr = rows_of(p.res, p.ldr, p.res_f32 ? 4 : 2), rh = rows_of(p.out_half, p.ldo, 2),
+                                     rf = rows_of(p.out_f32, p.ldo, 4);
+        const int vr = lane_at(p.ldr, p.res_f32 ? 4 : 2), vh = lane_at(p.ldo, 2), vf = lane_at(p.ldo, 4);
         uint2 early[ROWS / 4] = {};
-        if (direct && !p.res_f32) {
+        if (direct && p.res && !p.res_f32) {
 #pragma unroll
             for (int k = 0; k < ROWS / 4; k++)
-                early[k] = __builtin_bit_cast(uint2, __builtin_amdgcn_raw_buffer_load_b64(rr, rv, rowoff(k), 0));
+                early[k] = __builtin_bit_cast(uint2, __builtin_amdgcn_raw_buffer_load_b64(rr, vr, row_at(k, p.ldr, 2), 0));
         }
         auto put = [&](int row, const f32x4_t(&c)[4][4]) {
 #pragma unroll
@@ -542,50 +543,54 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(1, 1))) voi
             }
             continue;
         }
-        if (GATED || p.act != MOE_LINEAR_NONE || p.bias) {
-#pragma unroll 1
-            for (int r0 = q4; r0 < ROWS; r0 += 4 * R) {
-                float a[4 * R];
-                activated(r0, a);
-#pragma unroll
-                for (int i = 0; i < R; i++) *sums(r0 + 4 * i) = f32x4_t{a[4 * i], a[4 * i + 1], a[4 * i + 2], a[4 * i + 3]};
-            }
-        }
-        auto batch = [&](int b, const uint4(&res)[R]) {
-            int t[R];
-            float a[4 * R];
-#pragma unroll
-            for (int i = 0; i < R; i++) {
-                const int r = q4 + 4 * (b * R + i);
-                t[i] = token(r);
-                const f32x4_t c = *sums(r);
-#pragma unroll
-                for (int j = 0; j < 4; j++) a[4 * i + j] = c[j];
-            }
-            write_rows<F16, R>(p, t, n, a, res);
+        auto store = [&](int k, const f32x4_t &v) {
+            if (p.out_half)
+                __builtin_amdgcn_raw_buffer_store_b64(__builtin_bit_cast(u32x2_t, pack4<F16>(v[0], v[1], v[2], v[3])), rh, vh,
+                                                      row_at(k, p.ldo, 2), 0);
+            if (p.out_f32)
+                __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4_t, v), rf, vf, row_at(k, p.ldo, 4), 0);
         };
-        if (!p.res_f32) {
+        // the activation in a loop, so that its code is there once; back to
+        // LDS where the residual, in registers, waits for it
+        if (GATED || p.act != MOE_LINEAR_NONE) {
+#pragma unroll 1
+            for (int k = 0; k < ROWS / 4; k += R) {
+                float a[4 * R];
+                activated(q4 + 4 * k, a);
 #pragma unroll
-            for (int b = 0; b < BATCHES; b++) {
-                uint4 res[R];
-#pragma unroll
-                for (int i = 0; i < R; i++) res[i] = make_uint4(early[b * R + i].x, early[b * R + i].y, 0, 0);
-                batch(b, res);
-                __builtin_amdgcn_sched_barrier(0);
+                for (int i = 0; i < R; i++) {
+                    const f32x4_t v = {a[4 * i], a[4 * i + 1], a[4 * i + 2], a[4 * i + 3]};
+                    if (p.res) *sums(q4 + 4 * (k + i)) = v;
+                    else store(k + i, v);
+                }
             }
+            if (!p.res) continue;
+#pragma unroll
+            for (int j = 0; j < 4; j++) ba[j] = 0.0f;
+        }
+        auto write = [&](int k, float4 r) {
+            const f32x4_t c = *sums(q4 + 4 * k);
+            store(k, f32x4_t{c[0] + ba[0] + r.x, c[1] + ba[1] + r.y, c[2] + ba[2] + r.z, c[3] + ba[3] + r.w});
+        };
+        if (!p.res) {
+#pragma unroll
+            for (int k = 0; k < ROWS / 4; k++) write(k, make_float4(0.0f, 0.0f, 0.0f, 0.0f));
+        } else if (!p.res_f32) {
+#pragma unroll
+            for (int k = 0; k < ROWS / 4; k++)
+                write(k, make_float4(half_f32<F16>((uint16_t)early[k].x), half_f32<F16>((uint16_t)(early[k].x >> 16)),
+                                     half_f32<F16>((uint16_t)early[k].y), half_f32<F16>((uint16_t)(early[k].y >> 16))));
         } else {
-            constexpr int PART = BATCHES / 4;  // (fp32: a quarter of the rows at a time)
+            constexpr int PART = ROWS / 16;  // (fp32: a quarter of the rows at a time)
 #pragma unroll
             for (int q = 0; q < 4; q++) {
-                uint4 res[PART][R];
+                float4 res[PART];
 #pragma unroll
-                for (int b = 0; b < PART; b++)
+                for (int k = 0; k < PART; k++)
+                    res[k] = __builtin_bit_cast(
+                        float4, __builtin_amdgcn_raw_buffer_load_b128(rr, vr, row_at(q * PART + k, p.ldr, 4), 0));
 #pragma unroll
-                    for (int i = 0; i < R; i++)
-                        res[b][i] = __builtin_bit_cast(
-                            uint4, __builtin_amdgcn_raw_buffer_load_b128(rr, rv, rowoff((q * PART + b) * R + i), 0));
-#pragma unroll
-                for (int b = 0; b < PART; b++) batch(q * PART + b, res[b]);
+                for (int k = 0; k < PART; k++) write(q * PART + k, res[k]);
                 __builtin_amdgcn_sched_barrier(0);
             }
         }
