@@ -798,9 +798,25 @@ __global__ __launch_bounds__(WN * WT * 64) void k_linear_tile(LinearParams p, in
     wait_copies<0>();
     barrier();
 
-    // epilogue through the wave's own LDS: rows of tokens, EN sums of each half
+    // epilogue through the wave's own LDS: rows of tokens, EN sums of each
+    // half; a lane has four outputs of R rows of a half.  Every residual is
+    // loaded before the first store (a load waits for the stores before it).
     LDS uint8_t *buf = lds + wv * G::EWAVE;
-    constexpr int TR = TM / WT;
+    constexpr int TR = TM / WT, LPR = G::EN / 4, RPI = 64 / LPR, R = TR / RPI, HALVES = GATED ? 1 : 2;
+    static_assert(TR % RPI == 0, "rows");
+    const int c4 = (lane % LPR) * 4, row0 = lane / LPR;
+    int t[HALVES][R];
+    uint4 res[HALVES][R] = {};
+#pragma unroll
+    for (int h = 0; h < HALVES; h++) {
+        const int n = (h ? n1 : n0) + wn * G::EN + c4;
+#pragma unroll
+        for (int i = 0; i < R; i++) {
+            t[h][i] = t0 + wt * TR + row0 + i * RPI;
+            t[h][i] = t[h][i] < p.M && n < p.N ? t[h][i] : -1;
+        }
+        if (ksplit == 1) load_res<R>(p, t[h], n, res[h]);
+    }
 #pragma unroll
     for (int h = 0; h < 2; h++)
 #pragma unroll
@@ -808,34 +824,32 @@ __global__ __launch_bounds__(WN * WT * 64) void k_linear_tile(LinearParams p, in
 #pragma unroll
             for (int g = 0; g < G::FT; g++)
                 *reinterpret_cast<LDS f32x4_t *>(buf + (h * TR + g * 16 + r16) * G::EROW + f * 64 + q4 * 16) = acc[h * G::FN + f][g];
-    constexpr int LPR = G::EN / 4, RPI = 64 / LPR;  // lanes per row, rows per instruction
-    const int c4 = (lane % LPR) * 4;
-#pragma unroll 1
-    for (int h = 0; h < (GATED ? 1 : 2); h++) {
+    auto sums = [&](int h, int i) {
+        return *reinterpret_cast<const LDS f32x4_t *>(buf + (h * TR + row0 + i * RPI) * G::EROW + c4 * 4);
+    };
+#pragma unroll
+    for (int h = 0; h < HALVES; h++) {
         const int n = (h ? n1 : n0) + wn * G::EN + c4;
-        if (n >= p.N) continue;
-        float ba[4], bu[4] = {};
+        if (ksplit > 1) {
+#pragma unroll
+            for (int i = 0; i < R; i++)
+                if (t[h][i] >= 0) store_part<GATED>(p, ks, t[h][i], n, sums(h, i), sums(GATED ? 1 : h, i));
+            continue;
+        }
+        float a[4 * R], u[4 * R], ba[4], bu[4] = {};
         bias4<F16>(p.bias, p.bias_f32, n, p.N, ba);
         if (GATED) bias4<F16>(p.bias_up, p.bias_f32, n, p.N, bu);
-#pragma unroll 1
-        for (int r = lane / LPR; r < TR; r += RPI) {
-            const int t[1] = {t0 + wt * TR + r};
-            if (t[0] >= p.M) break;
-            const f32x4_t c = *reinterpret_cast<const LDS f32x4_t *>(buf + (h * TR + r) * G::EROW + c4 * 4);
-            f32x4_t d = {};
-            if (GATED) d = *reinterpret_cast<const LDS f32x4_t *>(buf + (TR + r) * G::EROW + c4 * 4);
-            if (ksplit > 1) {
-                store_part<GATED>(p, ks, t[0], n, c, d);
-                continue;
-            }
-            float a[4], u[4];
+#pragma unroll
+        for (int i = 0; i < R; i++) {
+            const f32x4_t c = sums(h, i), d = sums(GATED ? 1 : h, i);
 #pragma unroll
             for (int j = 0; j < 4; j++) {
-                a[j] = c[j] + ba[j];
-                u[j] = GATED ? d[j] + bu[j] : 0.0f;
+                a[4 * i + j] = c[j] + ba[j];
+                u[4 * i + j] = GATED ? d[j] + bu[j] : 0.0f;
             }
-            finish_row<F16, GATED>(p, t[0], n, a, u);
         }
+        activate<GATED>(a, u, p.act, p.b1, p.b2);
+        write_rows<F16, R>(p, t[h], n, a, res[h]);
     }
 }
 
