@@ -51,8 +51,8 @@ constexpr Kind kKinds[] = {
     {kTile128x128, 128, 128, 0, 470, false, true, false, 5500.0},
     {kBig, 256, 256, 0, 1270, false, true, false, 5500.0},
     {kAny64x32, 64, 32, 170, 345, true, true, true, 5500.0},
-    {kAny64x64, 64, 64, 300, 450, true, true, true, 5500.0},
-    {kAny128x128, 128, 128, 0, 820, false, true, true, 5500.0},
+    {kAny64x64, 64, 64, 200, 400, true, true, true, 5500.0},
+    {kAny128x128, 128, 128, 0, 890, false, true, true, 5500.0},
 };
 
 // The kernel and split of K of the least estimated time: a launch, the
