@@ -18,6 +18,14 @@
 // too close to tell apart in fp32, the token takes `whole`: all values as
 // doubles, k rounds of a wave-wide maximum.  A value of -inf marks an expert
 // that takes no part, and a NaN one ranks as +inf.
+//
+// What bounds it: 16384 tokens of 896 fp32 logits, k = 16, sigmoid with a
+// bias: 24.4 us with the counts, of which reading the logits is 11.9 at the
+// card's copy rate.  The rest is vector instructions, about 580 per token
+// (two transcendental ones per expert, the candidates' doubles), at the four
+// waves per SIMD that 128 registers allow: five waves with 96 cost more in
+// spills than they hide (28.4 us).  All values as doubles and k rounds of a
+// maximum took 175 us.  Up to a few hundred tokens it is the launches.
 #include <math.h>
 
 #include "common.h"
@@ -231,14 +239,20 @@ __device__ __forceinline__ float margin(bool by_logit, float t)
     return by_logit ? 4.8e-7f * fabsf(t) + 1e-9f : 4.8e-7f + 2.4e-7f * fabsf(t);
 }
 
-// the logits of a row that lane l holds: experts l, l + 64, ... (past the
-// end: the last one's), at `off` bytes
+// the logits of a row of E that lane l holds: experts l, l + 64, ...; past
+// the end 0 (a buffer's bounds: one address for all of them)
 template <int EPL, typename L>
-__device__ __forceinline__ void load_row(const L *row, const uint32_t (&off)[EPL], float (&l)[EPL])
+__device__ __forceinline__ void load_row(const L *row, int E, float (&l)[EPL])
 {
+    const __amdgpu_buffer_rsrc_t r = grsrc(row, (uint32_t)(E * sizeof(L)));
+    const int at = (threadIdx.x & 63) * (int)sizeof(L);
 #pragma unroll
-    for (int i = 0; i < EPL; i++)
-        l[i] = logit_f32<L>(*reinterpret_cast<const L *>(reinterpret_cast<const char *>(row) + off[i]));
+    for (int i = 0; i < EPL; i++) {
+        if constexpr (sizeof(L) == 4)
+            l[i] = __builtin_bit_cast(float, __builtin_amdgcn_raw_buffer_load_b32(r, at + i * 256, 0, 0));
+        else
+            l[i] = logit_f32<L>(__builtin_bit_cast(L, __builtin_amdgcn_raw_buffer_load_b16(r, at + i * 128, 0, 0)));
+    }
 }
 
 // the same lane number, but not known to be: what follows from it is computed
@@ -250,17 +264,19 @@ __device__ __forceinline__ int lane_here()
     return lane;
 }
 
-// The choices of one token from its logits l and their biases (-inf: no
+// The choices of one token from its logits l and the biases in LDS (-inf: no
 // expert, or one switched off; 0 without a bias).  l is free, and filled with
 // the logits of the row `next`, once the experts' values are known.
 template <int EPL, bool SOFT, bool by_logit, typename L>
-__device__ __forceinline__ Pick choose(const GateParams &p, const L *row, const L *next, const uint32_t (&off)[EPL],
-                                       float (&l)[EPL], const float (&bias)[EPL], GateLds<EPL> &lds)
+__device__ __forceinline__ Pick choose(const GateParams &p, const L *row, const L *next, float (&l)[EPL],
+                                       const float *biases, GateLds<EPL> &lds)
 {
     const int lane = lane_here();
     const float ninf = -INFINITY;
     GateCands &w = lds.n;
-    float a[EPL];
+    float a[EPL], bias[EPL];
+#pragma unroll
+    for (int i = 0; i < EPL; i++) bias[i] = biases[lane + 64 * i];
     float m = ninf;
     double sum = 1.0;
     if (SOFT) {
@@ -300,7 +316,7 @@ __device__ __forceinline__ Pick choose(const GateParams &p, const L *row, const 
             for (int i = 0; i < EPL; i++) a[i] = a[i] != ninf ? (float)INFINITY : ninf;
         }
     }
-    load_row<EPL, L>(next, off, l);
+    load_row<EPL, L>(next, p.E, l);
     // logits between which every two have different scores as doubles (the
     // sigmoid's reach 1, and both scores 0, further out)
     const float high = !by_logit || SOFT ? (float)INFINITY : 20.0f;
@@ -368,7 +384,7 @@ __device__ __forceinline__ Pick choose(const GateParams &p, const L *row, const 
     const bool there = lane < n;
     const int id = there ? w.id[lane] : 0;
     const double s = score_of<SOFT>(logit_f32<L>(row[id]), m, sum);
-    double c = s + (p.bias ? (double)p.bias[id] : 0.0);
+    double c = s + (double)biases[id];
     c = there ? (c != c ? (double)INFINITY : c) : -(double)INFINITY;
     w.c[lane] = c;
     __builtin_amdgcn_wave_barrier();
@@ -405,23 +421,17 @@ __global__ __launch_bounds__(kGateWaves * 64) __attribute__((amdgpu_waves_per_eu
     } else if (p.counts && blockIdx.x == 0) {
         for (int e = threadIdx.x; e < p.E; e += kGateWaves * 64) p.counts[e] = 0;
     }
-    float bias[EPL];
-#pragma unroll
-    for (int i = 0; i < EPL; i++) {
-        const int e = lane + 64 * i;
-        bias[i] = e < p.E ? (p.bias ? p.bias[e] : 0.0f) : -INFINITY;
-    }
+    __shared__ float bias[64 * EPL];  // (-inf past the end)
+    for (int e = threadIdx.x; e < 64 * EPL; e += kGateWaves * 64) bias[e] = e < p.E ? (p.bias ? p.bias[e] : 0.0f) : -INFINITY;
+    __syncthreads();
     const L *logits = reinterpret_cast<const L *>(p.logits);
     float l[EPL];
-    uint32_t off[EPL];
-#pragma unroll
-    for (int i = 0; i < EPL; i++) off[i] = (uint32_t)min(lane + 64 * i, p.E - 1) * (uint32_t)sizeof(L);
     int t = blockIdx.x * kGateWaves + wv;
-    load_row<EPL, L>(logits + (size_t)min(t, p.T - 1) * p.ld, off, l);
+    load_row<EPL, L>(logits + (size_t)min(t, p.T - 1) * p.ld, p.E, l);
     for (; t < p.T; t += gridDim.x * kGateWaves) {
         const L *row = logits + (size_t)t * p.ld;
         const L *next = logits + (size_t)min(t + (int)gridDim.x * kGateWaves, p.T - 1) * p.ld;
-        const Pick c = choose<EPL, SOFT, BY_LOGIT, L>(p, row, next, off, l, bias, lds[wv]);
+        const Pick c = choose<EPL, SOFT, BY_LOGIT, L>(p, row, next, l, bias, lds[wv]);
         double w = c.s;
         if (p.renorm) {
             const double total = wave_sum64(lane < p.k ? c.s : 0.0);
@@ -462,7 +472,10 @@ __global__ __launch_bounds__(1024) void k_gate_count(GateParams p)
     }
 }
 
-constexpr int kGateBlocks = 1024;  // blocks at most; more tokens take turns
+// blocks at most, two per CU; more tokens take turns, a row's logits loaded
+// while the one before is chosen from (16384x896: 24.4 us, with 1024 blocks
+// 25.6, with 2048 28.2)
+constexpr int kGateBlocks = 512;
 constexpr int kCountPart = 4096;   // choices that a counting block takes
 
 template <int EPL, bool SOFT, bool BY_LOGIT, typename L>
