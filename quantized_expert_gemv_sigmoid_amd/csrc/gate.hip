@@ -104,15 +104,21 @@ __device__ __forceinline__ double wave_sum64(double v)
 }
 __device__ __forceinline__ double wave_max64(double v)
 {
-#pragma unroll
-    for (int m = 32; m >= 1; m >>= 1) v = fmax(v, __shfl_xor(v, m, 64));
-    return v;
+    v = fmax(v, dpp_d<0xB1>(v));
+    v = fmax(v, dpp_d<0x4E>(v));
+    v = fmax(v, dpp_d<0x141>(v));
+    v = fmax(v, dpp_d<0x140>(v));
+    v = fmax(v, __shfl_xor(v, 16, 64));
+    return fmax(v, __shfl_xor(v, 32, 64));
 }
 __device__ __forceinline__ int wave_min(int v)
 {
-#pragma unroll
-    for (int m = 32; m >= 1; m >>= 1) v = min(v, __shfl_xor(v, m, 64));
-    return v;
+    v = min(v, __builtin_amdgcn_update_dpp(0, v, 0xB1, 0xF, 0xF, true));
+    v = min(v, __builtin_amdgcn_update_dpp(0, v, 0x4E, 0xF, 0xF, true));
+    v = min(v, __builtin_amdgcn_update_dpp(0, v, 0x141, 0xF, 0xF, true));
+    v = min(v, __builtin_amdgcn_update_dpp(0, v, 0x140, 0xF, 0xF, true));
+    v = min(v, __shfl_xor(v, 16, 64));
+    return min(v, __shfl_xor(v, 32, 64));
 }
 __device__ __forceinline__ int below(uint64_t mask)  // set bits below this lane
 {
@@ -184,15 +190,23 @@ __device__ __forceinline__ bool group_stays(const GateParams &p, const T *v, T &
 
 // everything as doubles in LDS, k rounds of a maximum
 template <bool SOFT, typename L>
-__device__ __forceinline__ Pick whole(const GateParams &p, const L *row, double *v, float m, double sum)
+__device__ __forceinline__ Pick whole(const GateParams &p, const L *row, const float *biases, double *v, float m, double sum)
 {
     const int lane = threadIdx.x & 63;
     const double ninf = -INFINITY;
 #pragma unroll 1
-    for (int e = lane; e < p.E; e += 64) {
-        const float l = logit_f32<L>(row[e]), b = p.bias ? p.bias[e] : 0.0f;
-        const double x = score_of<SOFT>(l, m, sum) + b;
-        v[e] = l != -INFINITY && b != -INFINITY ? (x != x ? (double)INFINITY : x) : ninf;
+    for (int e0 = lane; e0 < p.E; e0 += 256) {  // (four logits on the way at a time)
+        float l4[4];
+#pragma unroll
+        for (int i = 0; i < 4; i++) l4[i] = logit_f32<L>(row[min(e0 + 64 * i, p.E - 1)]);
+#pragma unroll
+        for (int i = 0; i < 4; i++) {
+            const int e = e0 + 64 * i;
+            if (e >= p.E) break;
+            const float l = l4[i], b = biases[e];
+            const double x = score_of<SOFT>(l, m, sum) + b;
+            v[e] = l != -INFINITY && b != -INFINITY ? (x != x ? (double)INFINITY : x) : ninf;
+        }
     }
     __builtin_amdgcn_wave_barrier();
     uint64_t kept = ~0ull;
@@ -208,7 +222,7 @@ __device__ __forceinline__ Pick whole(const GateParams &p, const L *row, double 
     for (int j = 0; j < p.k; j++) {
         if (look) {
             best = ninf;
-#pragma unroll 1
+#pragma unroll 4
             for (int e = lane; e < p.E; e += 64) {
                 const double x = v[e];
                 const bool more = x > best && (p.groups == 1 || ((kept >> group_of(p, e)) & 1));  // (strict: the lower id of a tie)
@@ -377,7 +391,7 @@ __device__ __forceinline__ Pick choose(const GateParams &p, const L *row, const 
         set &= ~(1u << top);
         n += __builtin_popcountll(mask);
     }
-    if (slow || n > 64) return whole<SOFT, L>(p, row, lds.v, m, sum);
+    if (slow || n > 64) return whole<SOFT, L>(p, row, biases, lds.v, m, sum);
     // (one wave: its LDS accesses are performed in issue order)
     __builtin_amdgcn_wave_barrier();
     // candidate `lane`, its score and selection value
