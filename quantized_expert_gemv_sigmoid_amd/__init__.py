@@ -395,6 +395,10 @@ def _same_device(first, *others) -> None:
             raise MoeError(EINVAL, f"tensors on {d} and {t.device}")
 
 
+def _ws_tensor(ws) -> tuple:
+    return () if ws is None or isinstance(ws, tuple) else (ws,)
+
+
 def _call(x, stream, f, *args) -> int:
     """f(*args, stream) on x's device: that device's current stream where none is given."""
     i = x.device.index
@@ -436,9 +440,18 @@ def gate(desc: GateDesc, logits, T: int, ids, weights, counts=None, stream=None)
 
 def route_gated(desc: LayerDesc, gate_desc: GateDesc, x, T: int, ids, weights, counts, ws,
                 stream=None) -> None:
+    """moe_route_gated on the first T rows of x ([.., d_model], contiguous bfloat16 or their bits)."""
+    if _torch is None:
+        _setup()
+    E, n = desc.n_experts, T * desc.top_k
+    if x.dtype not in (_torch.bfloat16, _torch.int16):
+        raise MoeError(EINVAL, f"x: {x.dtype}")
+    _same_device(x, ids, weights, counts, *_ws_tensor(ws))
     wp, wn = _ws(ws)
-    _check(lib().moe_route_gated(ctypes.byref(desc), ctypes.byref(gate_desc), _ptr(x), T, _ptr(ids),
-                                 _ptr(weights), _ptr(counts), wp, wn, _stream(stream)), "moe_route_gated")
+    i32 = _torch.int32
+    _check(_call(x, stream, lib().moe_route_gated, desc, gate_desc, _flat(x, T * desc.d_model, x.dtype, "x"), T,
+                 _flat(ids, n, i32, "ids"), _flat(weights, n, _torch.float32, "weights"), _flat(counts, E, i32, "counts"),
+                 wp, wn), "moe_route_gated")
 
 
 def make_linear_desc(w, w_up=None, bias=None, bias_up=None, act: int = LINEAR_NONE,
@@ -486,7 +499,7 @@ def linear(desc: LinearDesc, x, T: int, out_half, out_f32, out_mode: int, ws, re
     n, half = desc.n_out, desc.type
     if _type_of(x) != half:
         raise MoeError(EINVAL, f"x: {x.dtype}")
-    _same_device(x, out_half, out_f32, residual)
+    _same_device(x, out_half, out_f32, residual, *_ws_tensor(ws))
     ldo = ldr = op = fp = rp = None
     if out_mode != OUT_F32 and out_half is not None:
         if _type_of(out_half) != half:

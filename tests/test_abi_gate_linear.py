@@ -186,3 +186,22 @@ def test_binding_refuses_mismatched_tensors(L):
                dict(residual=torch.empty(3, 5)), dict(residual=o[:, :4])):
         with pytest.raises(moe.MoeError):
             moe.linear(ld, **{**dict(x=x, T=3, out_half=o, out_f32=None, out_mode=moe.OUT_HALF, ws=(256, 1 << 30)), **kw})
+
+
+def test_binding_refuses_mismatched_tensors_of_a_routing_call(L):
+    layer, g = moe.LayerDesc(), moe.make_gate_desc(8, 2)
+    layer.n_experts, layer.top_k, layer.d_model = 8, 2, 256
+    good = dict(x=torch.empty(3, 256, dtype=torch.bfloat16), T=3, ids=torch.empty(3, 2, dtype=torch.int32),
+                weights=torch.empty(3, 2), counts=torch.empty(8, dtype=torch.int32), ws=torch.empty(256, dtype=torch.uint8))
+    for kw in (dict(x=good["x"].float()), dict(x=good["x"].half()), dict(x=good["x"][:2]), dict(x=good["x"][:, ::2]), dict(ids=good["ids"].long()),
+               dict(ids=good["ids"][:2]), dict(weights=good["weights"].half()), dict(counts=good["counts"][:7]),
+               dict(ws=torch.empty(256, dtype=torch.uint8, device="meta")), dict()):  # (the last: not a GPU's)
+        with pytest.raises(moe.MoeError):
+            moe.route_gated(layer, g, **{**good, **kw})
+
+
+def test_binding_refuses_a_workspace_of_another_device(L):
+    w = torch.empty(5, 8, dtype=torch.bfloat16)
+    with pytest.raises(moe.MoeError, match="tensors on"):
+        moe.linear(moe.make_linear_desc(w), torch.empty(3, 8, dtype=torch.bfloat16), 3, torch.empty(3, 5, dtype=torch.bfloat16),
+                   None, moe.OUT_HALF, torch.empty(256, dtype=torch.uint8, device="meta"))

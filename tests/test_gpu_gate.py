@@ -272,3 +272,39 @@ def test_route_gated_and_experts(T):
         h = gl.host
         o = oracle.forward(x, ids.cpu().numpy(), w.cpu().numpy(), oracle.held_arrays(h), oracle.shared_arrays(h))
         assert_close(out.cpu().numpy(), o, f"experts T={T}")
+
+
+def test_calls_of_two_streams_at_once():
+    """Two streams' calls of different sizes, several deep, each with its own outputs: each as alone."""
+    g = torch.Generator(device="cuda").manual_seed(17)
+    sides = []
+    for T, E, k, kw in ((700, 896, 16, {}), (1900, 60, 4, dict(score=moe.SCORE_SOFTMAX, n_groups=6, top_groups=3))):
+        l = torch.randn(T, E, device="cuda", generator=g)
+        sides.append((moe.make_gate_desc(E, k, **kw), l, T, [torch.empty(T, k, dtype=torch.int32, device="cuda") for _ in range(2)],
+                      [torch.empty(T, k, device="cuda") for _ in range(2)],
+                      [torch.empty(E, dtype=torch.int32, device="cuda") for _ in range(2)]))
+    for d, l, T, ids, w, c in sides:
+        moe.gate(d, l, T, ids[0], w[0], c[0])
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in sides]
+    for _ in range(10):
+        for s, (d, l, T, ids, w, c) in zip(streams, sides):
+            moe.gate(d, l, T, ids[1], w[1], c[1], stream=s)
+    torch.cuda.synchronize()
+    for _, _, _, ids, w, c in sides:
+        assert torch.equal(ids[0], ids[1]) and torch.equal(w[0], w[1]) and torch.equal(c[0], c[1])
+
+
+def test_rows_past_two_gib():
+    """Rows a wide distance apart, the last ones past 2^31 and 2^32 bytes."""
+    T, E, ld = 520, 64, 1 << 21
+    buf = torch.zeros(T * ld, device="cuda")
+    l = torch.randn(T, E, device="cuda")
+    rows = buf.view(T, ld)[:, :E]
+    rows.copy_(l)
+    d = moe.make_gate_desc(E, 6)
+    out = [(torch.empty(T, 6, dtype=torch.int32, device="cuda"), torch.empty(T, 6, device="cuda")) for _ in range(2)]
+    for (ids, w), logits in zip(out, (l, rows)):
+        moe.gate(d, logits, T, ids, w)
+    torch.cuda.synchronize()
+    assert torch.equal(out[0][0], out[1][0]) and torch.equal(out[0][1], out[1][1])
