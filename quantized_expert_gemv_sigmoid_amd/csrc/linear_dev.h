@@ -4,7 +4,15 @@
 //
 // Every kernel multiplies D[n][t] = w x^T on the matrix cores with fp32 sums:
 // the weights are the A operand, so a lane ends with four consecutive n of
-// one token.
+// one token.  K comes in stages of 64 into LDS rows of 128 bytes, their
+// 16-byte pieces permuted (piece ^ row / 2) so that fragment reads touch every
+// bank alike.  Four kernels, by what bounds them (which call takes which:
+// linear.hip):
+//   k_linear_big   the matrix cores: 256 x 256 tiles
+//   k_linear_tile  LDS reads and latency: 64 x 32 to 128 x 128 tiles
+//   k_linear_few   the weights' way from memory, each row read once: 16 rows
+//                  x 8 to 32 tokens
+//   k_linear_join  sums of a K split over blocks
 #pragma once
 
 #include <math.h>
@@ -304,6 +312,19 @@ constexpr int kBigRow = 64 * 4 + 16;        // a row of the epilogue's buffer
 constexpr int kBigWave = 128 * kBigRow;  // a wave's part of it
 constexpr int kBigLds = 4 * kBigWave > kBigRing ? 4 * kBigWave : kBigRing;
 
+// 256 x 256 outputs (gated: 128 of each matrix) per block and CU, four waves
+// of 128 x 128, one to a SIMD, whose 256 sums per lane fill the accumulation
+// registers: 64 products of 16 x 16 x 32 per 32 fragment reads of 16 bytes,
+// so LDS supplies half of what it could, and the matrix cores are the bound.
+// 16 x 16 x 32 and not 32 x 32 x 16: on registers alone the whole chip does
+// 2050 TFLOP/s with the former and 1660-1850 with the latter, which draws
+// more power (4096 x 7168 x 7168: 372 us with the latter, 325 with the former).
+// Measured: 4096 x 7168 x 7168 296 us (1422 TFLOP/s, the library's product
+// 285-290), with bias and a 16-bit residual 315; 4096 x 3584 x 2 x 6144
+// SwiGLU 251, SiTU-GLU 278.  Matrix cores busy for 76% of the kernel; 8192^3
+// reaches 1491 TFLOP/s, where clocks give way to power.  The rest is the last
+// turn of tiles (448 on 256 CUs) and the epilogue, which nothing overlaps as
+// a CU holds one block.
 template <bool F16, bool GATED>
 __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(1, 1))) void k_linear_big(LinearParams p, int tn,
                                                                                                int tt, int ksplit)
@@ -605,7 +626,16 @@ __device__ __forceinline__ f32x4_t mfma16v(f16x8_t a, f16x8_t b, f32x4_t c)
 }
 
 // TN weight rows (gated: TN / 2 of each matrix) x TM tokens per block, K in a
-// ring of NST stages of 64; WN x WT waves.
+// ring of NST stages of 64; WN x WT waves.  Each wave holds fragments a step
+// ahead of its products.  The 128 x 128 tile is bound by LDS (16 KB of
+// fragments per 2 MFLOP at 128 bytes a clock: 0.47 us a stage against 0.3 of
+// products), the small ones by a stage's latency (the ring's length beyond
+// three stages changes nothing: 24 x 3584 x 6144 12.4 us with three and six).
+// Measured: 200 x 3584 x 7168 (128 x 64) 19.4 us with the weights from
+// memory (library 24), 4096 x 7168 x 896 to fp32 (128 x 128) 48 us, 53-66 with
+// x from memory (54, 64), 24 x 3584 x 2 x 6144 (64 x 32) 16.2, which is 5440
+// GB/s of weights.  Rows that are not 16-byte aligned (ANY) go through
+// registers: 333 x 1117 x 2049 14 us (library 20), 2048 x 3585 x 3587 86 (75).
 template <int TN, int TM, int WN, int WT, int NST>
 struct Tile {
     static constexpr int NW = WN * WT, THREADS = NW * 64;
@@ -849,7 +879,9 @@ __global__ __launch_bounds__(WN * WT * 64) void k_linear_tile(LinearParams p, in
     }
 }
 
-// sums of the K parts, in their order, and the epilogue: a thread per four outputs
+// sums of the K parts, in their order, and the epilogue: a thread per four
+// outputs.  A launch of its own (about 2 us) and not the last block's work:
+// the sums keep their order, and no counter has to be cleared.
 template <bool F16, bool GATED, int KS>
 __global__ __launch_bounds__(256) void k_linear_join(LinearParams p)
 {
@@ -884,7 +916,10 @@ __global__ __launch_bounds__(256) void k_linear_join(LinearParams p)
 // A block multiplies 16 weight rows (gated: 16 of each matrix) with 8 XP
 // tokens; each of its eight waves takes an eighth of K through a ring of NST
 // stages of 64 in LDS of its own, filled by direct copies, so no wave waits
-// for another until the sums join.  Tokens past the end are zeros.
+// for another until the sums join.  Tokens past the end are zeros.  Bound by
+// the weights' way from memory: 1 x 7168 x 3584 10.0 us, 5140 GB/s, the rate
+// of a large copy (the first kernel, a wave per row without LDS, took 91).
+// One stage more in the ring takes the same time.
 constexpr int kFewWaves = 8;
 
 template <bool GATED, int XP, int NST>
