@@ -21,7 +21,7 @@
 //
 // What bounds it: 16384 tokens of 896 fp32 logits, k = 16, sigmoid with a
 // bias: 24.4 us with the counts, of which reading the logits is 11.9 at the
-// card's copy rate.  The rest is vector instructions, about 580 per token
+// card's copy rate.  The rest is vector instructions, about 500 per token
 // (two transcendental ones per expert, the candidates' doubles), at the four
 // waves per SIMD that 128 registers allow: five waves with 96 cost more in
 // spills than they hide (28.4 us).  All values as doubles and k rounds of a

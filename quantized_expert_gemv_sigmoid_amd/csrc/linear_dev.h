@@ -321,7 +321,7 @@ constexpr int kBigLds = 4 * kBigWave > kBigRing ? 4 * kBigWave : kBigRing;
 // more power (4096 x 7168 x 7168: 372 us with the latter, 325 with the former).
 // Measured: 4096 x 7168 x 7168 296 us (1422 TFLOP/s, the library's product
 // 285-290), with bias and a 16-bit residual 315; 4096 x 3584 x 2 x 6144
-// SwiGLU 251, SiTU-GLU 278.  Matrix cores busy for 76% of the kernel; 8192^3
+// SwiGLU 251, SiTU-GLU 273-284.  Matrix cores busy for 76% of the kernel; 8192^3
 // reaches 1491 TFLOP/s, where clocks give way to power.  The rest is the last
 // turn of tiles (448 on 256 CUs) and the epilogue, which nothing overlaps as
 // a CU holds one block.
