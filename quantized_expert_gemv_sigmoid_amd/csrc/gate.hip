@@ -158,9 +158,10 @@ union GateLds {
 
 // Lane g < groups: whether group g stays, of the values v[E] in LDS.  P lanes
 // to a group: each takes every P-th of its experts, then their two largest
-// join.  `mine`: lane g's group value.
+// join.  `mine`: lane g's group value; `terms`: the magnitudes of what it is
+// the sum of, 0 for an infinite one (those are exact).
 template <typename T>
-__device__ __forceinline__ bool group_stays(const GateParams &p, const T *v, T &mine)
+__device__ __forceinline__ bool group_stays(const GateParams &p, const T *v, T &mine, T &terms)
 {
     const T ninf = -INFINITY;
     const int lane = threadIdx.x & 63, size = p.E / p.groups, P = 1 << (31 - __builtin_clz(64 / p.groups));
@@ -178,8 +179,9 @@ __device__ __forceinline__ bool group_stays(const GateParams &p, const T *v, T &
         v2 = fmax(fmax(v2, o2), fmin(v1, o1));
         v1 = fmax(v1, o1);
     }
-    const T value = p.top2 ? v1 + (v2 == ninf ? (T)0 : v2) : v1;
-    mine = __shfl(value, min(lane * P, 63), 64);
+    v2 = p.top2 && v2 != ninf ? v2 : (T)0;
+    mine = __shfl(v1 + v2, min(lane * P, 63), 64);
+    terms = __shfl(fabs(v1) == -ninf ? (T)0 : fabs(v1) + fabs(v2), min(lane * P, 63), 64);
     int rank = 0;
     for (int i = 0; i < p.groups; i++) {
         const T o = __shfl(mine, i, 64);
@@ -211,8 +213,8 @@ __device__ __forceinline__ Pick whole(const GateParams &p, const L *row, const f
     __builtin_amdgcn_wave_barrier();
     uint64_t kept = ~0ull;
     if (p.groups > 1) {
-        double value;
-        kept = __builtin_amdgcn_ballot_w64(group_stays<double>(p, v, value));
+        double value, terms;
+        kept = __builtin_amdgcn_ballot_w64(group_stays<double>(p, v, value, terms));
     }
     Pick mine = {-1, 0.0};
     double best = ninf;  // the lane's largest, and whose it is
@@ -343,12 +345,18 @@ __device__ __forceinline__ Pick choose(const GateParams &p, const L *row, const 
         for (int i = 0; i < EPL; i++)
             if (lane + 64 * i < p.E) v[lane + 64 * i] = a[i];
         __builtin_amdgcn_wave_barrier();
-        float mine;
-        const bool keep = group_stays<float>(p, v, mine), drop = lane < p.groups && !keep;
+        float mine, terms;
+        const bool keep = group_stays<float>(p, v, mine, terms), drop = lane < p.groups && !keep;
         const uint64_t kept = __builtin_amdgcn_ballot_w64(keep);
-        const float in = -wave_max(keep ? -mine : ninf), out = wave_max(drop ? mine : ninf);  // the last kept, the first not
-        // (two values, each the sum of up to two with a margin)
-        slow = out != ninf && (!(in - out > 4.0f * margin(by_logit, fmaxf(fabsf(in), fabsf(out)))) || out > high || in < low);
+        // Every group's value within its bounds: the margins of its one or two
+        // terms, whose own sizes count (two that cancel leave a sum near 0).
+        // Of a term's 2.4e-7 |v| its rounding takes 0.6e-7, the sum's as much,
+        // the bound's as much; a finite sum past fp32 may be anything.
+        const float err = by_logit ? 2.0f * margin(true, terms) : margin(false, terms) + (p.top2 ? 4.8e-7f : 0.0f);
+        const bool known = terms < INFINITY;
+        const float least = known ? mine - err : ninf, most = known ? mine + err : INFINITY;
+        const float in = -wave_max(keep ? -least : ninf), out = wave_max(drop ? most : ninf);  // the last kept, the first not
+        slow = out != ninf && (!(in > out) || out > high || in < low);
 #pragma unroll
         for (int i = 0; i < EPL; i++) a[i] = (kept >> (group_of(p, lane + 64 * i) & 63)) & 1 ? a[i] : ninf;
         __builtin_amdgcn_wave_barrier();
