@@ -459,6 +459,7 @@ __global__ __launch_bounds__(kGateWaves * 64) __attribute__((amdgpu_waves_per_eu
             const double total = wave_sum64(lane < p.k ? c.s : 0.0);
             w = total != 0.0 ? w / total : w;
         }
+        if (c.id < 0) w = 0.0;  // (a place left: also where the sum is NaN)
         if (lane < p.k) {
             p.ids[(size_t)t * p.k + lane] = c.id;
             p.weights[(size_t)t * p.k + lane] = (float)(w * (double)p.scale);
