@@ -412,6 +412,7 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(1, 1))) voi
         readA(a0, A0, i);
         readB(b0, B0, i);
     }
+    wait_copies<24>();  // (these reads too: the first two phases fill the units anew)
 
     // A phase multiplies one A half with one B half (64 n x 64 tokens x 64 k
     // per wave: 32 products).  Spread between them go the reads of the half
