@@ -406,11 +406,13 @@ typedef struct {
 size_t moe_linear_workspace_bytes(const moe_linear_desc *desc, int32_t max_tokens);
 
 /*
- * x: T rows of n_in values, ldx (n_in .. 2^22) elements apart.  residual:
- * NULL, or T rows of n_out values, ldr elements apart, ldr >= n_out or 0 (the
- * same row for every token).  out_mode: MOE_OUT_BF16 writes out_half (the
- * 16-bit output, in desc->type), MOE_OUT_F32 out_f32, MOE_OUT_BOTH both; rows
- * ldo >= n_out elements apart, the elements between them left as they are.
+ * x: T rows of n_in values, ldx >= n_in elements apart.  residual: NULL, or T
+ * rows of n_out values, ldr elements apart, ldr >= n_out or 0 (the same row
+ * for every token).  out_mode: MOE_OUT_BF16 writes out_half (the 16-bit
+ * output, in desc->type), MOE_OUT_F32 out_f32, MOE_OUT_BOTH both; rows ldo >=
+ * n_out elements apart, the elements between them left as they are.  ldx, ldr
+ * and ldo go up to 2^22 (MOE_EUNSUPPORTED above) where there are two rows or
+ * more; a single row may lie in rows of any length.
  * An output may be the residual's own buffer (same pointer, row distance and
  * type); otherwise outputs must not overlap inputs.
  */

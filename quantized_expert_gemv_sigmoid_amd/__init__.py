@@ -372,11 +372,11 @@ def _type_of(t) -> int:
 
 
 def _rows(t, rows: int, cols: int, what: str) -> int:
-    """Elements between the rows of a tensor of at least `rows` rows of `cols` contiguous values."""
+    """Elements between the rows of a tensor of at least `rows` rows of `cols` contiguous values (one row has none: cols)."""
     shape, stride = t.shape, t.stride()
     if len(shape) != 2 or shape[0] < rows or shape[1] != cols or (stride[1] != 1 and cols > 1):
         raise MoeError(EINVAL, f"{what}: {rows} rows of {cols} contiguous values wanted, got {tuple(shape)}, strides {tuple(stride)}")
-    return stride[0] if rows > 1 or stride[0] > cols else cols
+    return stride[0] if rows > 1 else cols
 
 
 def _flat(t, n: int, dtype, what: str):

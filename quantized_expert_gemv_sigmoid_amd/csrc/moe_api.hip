@@ -775,6 +775,10 @@ moe_status moe_linear(const moe_linear_desc *desc, const void *x, int64_t ldx, i
     if (st != MOE_OK) return st;
     if (T < 0 || ldx < desc->n_in || ldo < desc->n_out) return MOE_EINVAL;
     if (residual && ldr != 0 && ldr < desc->n_out) return MOE_EINVAL;
+    if (T == 1) {  // (no second row: whatever its distance)
+        ldx = desc->n_in;
+        ldo = ldr = desc->n_out;
+    }
     if (out_mode != MOE_OUT_BF16 && out_mode != MOE_OUT_F32 && out_mode != MOE_OUT_BOTH) return MOE_EINVAL;
     if (T > kMaxTokens || ldx > kMaxLd || ldo > kMaxLd || (residual && ldr > kMaxLd)) return MOE_EUNSUPPORTED;
     if (T == 0) return MOE_OK;
