@@ -86,6 +86,7 @@ class GateDesc(ctypes.Structure):
         ("group_score", ctypes.c_int32), ("renorm", ctypes.c_int32),
         ("routed_scale", ctypes.c_float), ("bias", ctypes.c_void_p),
     ]
+    device = None  # of the tensors that make_gate_desc was given
 
 
 class LinearDesc(ctypes.Structure):
@@ -97,6 +98,7 @@ class LinearDesc(ctypes.Structure):
         ("w", ctypes.c_void_p), ("w_up", ctypes.c_void_p),
         ("bias", ctypes.c_void_p), ("bias_up", ctypes.c_void_p),
     ]
+    device = None  # of the tensors that make_linear_desc was given
 
 
 _lib = None
@@ -388,8 +390,11 @@ def _flat(t, n: int, dtype, what: str):
     return t.data_ptr()
 
 
-def _same_device(first, *others) -> None:
+def _same_device(desc, first, *others) -> None:
+    """The tensors of a call lie on one device, and those of the descriptor (desc.device, where known) too."""
     d = first.device
+    if desc is not None and desc.device is not None and desc.device != d:
+        raise MoeError(EINVAL, f"tensors on {desc.device} and {d}")
     for t in others:
         if t is not None and t.device != d:
             raise MoeError(EINVAL, f"tensors on {d} and {t.device}")
@@ -422,7 +427,8 @@ def make_gate_desc(n_experts: int, top_k: int, score: int = SCORE_SIGMOID, bias=
     d.renorm, d.routed_scale = renorm, routed_scale
     if bias is not None and _type_of(bias) != F32:
         raise MoeError(EINVAL, f"bias: {bias.dtype}")
-    d.bias = None if bias is None else _flat(bias, n_experts, bias.dtype, "bias")
+    if bias is not None:
+        d.bias, d.device = _flat(bias, n_experts, bias.dtype, "bias"), bias.device
     return d
 
 
@@ -431,7 +437,7 @@ def gate(desc: GateDesc, logits, T: int, ids, weights, counts=None, stream=None)
     rows may be apart)."""
     E, n = desc.n_experts, T * desc.top_k
     ty = _type_of(logits)
-    _same_device(logits, ids, weights, counts)
+    _same_device(desc, logits, ids, weights, counts)
     i32 = _torch.int32
     _check(_call(logits, stream, lib().moe_gate, desc, logits.data_ptr(), ty, _rows(logits, T, E, "logits"), T,
                  _flat(ids, n, i32, "ids"), _flat(weights, n, _torch.float32, "weights"), _flat(counts, E, i32, "counts")),
@@ -446,7 +452,7 @@ def route_gated(desc: LayerDesc, gate_desc: GateDesc, x, T: int, ids, weights, c
     E, n = desc.n_experts, T * desc.top_k
     if x.dtype not in (_torch.bfloat16, _torch.int16):
         raise MoeError(EINVAL, f"x: {x.dtype}")
-    _same_device(x, ids, weights, counts, *_ws_tensor(ws))
+    _same_device(gate_desc, x, ids, weights, counts, *_ws_tensor(ws))
     wp, wn = _ws(ws)
     i32 = _torch.int32
     _check(_call(x, stream, lib().moe_route_gated, desc, gate_desc, _flat(x, T * desc.d_model, x.dtype, "x"), T,
@@ -467,13 +473,13 @@ def make_linear_desc(w, w_up=None, bias=None, bias_up=None, act: int = LINEAR_NO
     if d.type == F32:
         raise MoeError(EINVAL, f"w: {w.dtype}")
     d.ldw = _rows(w, n, k, "w")
-    _same_device(w, w_up, bias, bias_up)
+    _same_device(None, w, w_up, bias, bias_up)
     if w_up is not None and (w_up.dtype != w.dtype or _rows(w_up, n, k, "w_up") != d.ldw or w_up.shape != w.shape):
         raise MoeError(EINVAL, "w_up: not laid out as w")
     b = bias if bias is not None else bias_up
     d.bias_type = d.type if b is None else _type_of(b)
     d.residual_type = d.type if residual_type is None else residual_type
-    d.w, d.w_up = w.data_ptr(), None if w_up is None else w_up.data_ptr()
+    d.w, d.w_up, d.device = w.data_ptr(), None if w_up is None else w_up.data_ptr(), w.device
     d.bias = None if bias is None else _flat(bias, n, b.dtype, "bias")
     d.bias_up = None if bias_up is None else _flat(bias_up, n, b.dtype, "bias_up")
     return d
@@ -499,7 +505,7 @@ def linear(desc: LinearDesc, x, T: int, out_half, out_f32, out_mode: int, ws, re
     n, half = desc.n_out, desc.type
     if _type_of(x) != half:
         raise MoeError(EINVAL, f"x: {x.dtype}")
-    _same_device(x, out_half, out_f32, residual, *_ws_tensor(ws))
+    _same_device(desc, x, out_half, out_f32, residual, *_ws_tensor(ws))
     ldo = ldr = op = fp = rp = None
     if out_mode != OUT_F32 and out_half is not None:
         if _type_of(out_half) != half:
