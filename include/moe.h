@@ -405,6 +405,19 @@ typedef struct {
  * needed, nothing in it a caller reads. */
 size_t moe_linear_workspace_bytes(const moe_linear_desc *desc, int32_t max_tokens);
 
+/* The kernel that moe_linear takes for T >= 1 tokens whose rows start at x,
+ * ldx apart (its arguments), as a moe_linear_path + 256 * the parts that n_in
+ * is split into; a negative moe_status for a call it refuses.  Launches
+ * nothing and reads nothing behind the pointers.  ROWS16: 16 weight rows a
+ * block and 8, 16 or 32 tokens; TILE, ANY: weight rows x tokens, ANY where
+ * rows of x or w are not 16-byte aligned. */
+typedef enum {
+    MOE_LINEAR_ROWS16X8 = 0, MOE_LINEAR_ROWS16X16 = 1, MOE_LINEAR_ROWS16X32 = 2, MOE_LINEAR_TILE64X32 = 3,
+    MOE_LINEAR_TILE64X64 = 4, MOE_LINEAR_TILE128X64 = 5, MOE_LINEAR_TILE128X128 = 6, MOE_LINEAR_ANY64X32 = 7,
+    MOE_LINEAR_ANY64X64 = 8, MOE_LINEAR_ANY128X128 = 9, MOE_LINEAR_TILE256X256 = 10
+} moe_linear_path;
+int32_t moe_linear_path_for(const moe_linear_desc *desc, const void *x, int64_t ldx, int32_t T);
+
 /*
  * x: T rows of n_in values, ldx >= n_in elements apart.  residual: NULL, or T
  * rows of n_out values, ldr elements apart, ldr >= n_out or 0 (the same row

@@ -27,12 +27,14 @@ SCORE_SIGMOID, SCORE_SOFTMAX = 0, 1
 GROUP_MAX, GROUP_TOP2 = 0, 1
 (LINEAR_NONE, LINEAR_RELU, LINEAR_SILU, LINEAR_GELU, LINEAR_GELU_TANH, LINEAR_SITU_GLU,
  LINEAR_SWIGLU) = range(7)
+(LINEAR_ROWS16X8, LINEAR_ROWS16X16, LINEAR_ROWS16X32, LINEAR_TILE64X32, LINEAR_TILE64X64, LINEAR_TILE128X64,
+ LINEAR_TILE128X128, LINEAR_ANY64X32, LINEAR_ANY64X64, LINEAR_ANY128X128, LINEAR_TILE256X256) = range(11)
 
 EXPORTS = ("moe_workspace_bytes", "moe_path_for", "moe_route", "moe_expert_forward",
            "moe_layer", "moe_layer_noalloc", "moe_layer_timed", "moe_set_one_token_router_wait",
            "moe_latent_workspace_bytes", "moe_latent_path_for", "moe_latent_layer",
            "moe_latent_layer_timed", "moe_gate", "moe_route_gated", "moe_linear_workspace_bytes",
-           "moe_linear", "moe_status_str")
+           "moe_linear_path_for", "moe_linear", "moe_status_str")
 TIMED_EVENTS = 6
 NOALLOC_WS_BYTES = 128 << 20  # MOE_NOALLOC_WS_BYTES: the static workspace of moe_layer_noalloc
 
@@ -146,6 +148,8 @@ def lib() -> ctypes.CDLL:
         L.moe_route_gated.argtypes = [P, ctypes.POINTER(GateDesc), vp, i32, vp, vp, vp, vp, sz, vp]
         L.moe_linear_workspace_bytes.restype = sz
         L.moe_linear_workspace_bytes.argtypes = [ctypes.POINTER(LinearDesc), i32]
+        L.moe_linear_path_for.restype = i32
+        L.moe_linear_path_for.argtypes = [ctypes.POINTER(LinearDesc), vp, i64, i32]
         L.moe_linear.restype = i32
         L.moe_linear.argtypes = [ctypes.POINTER(LinearDesc), vp, i64, i32, vp, i64, vp, vp, i64, i32,
                                  vp, sz, vp]
@@ -496,6 +500,14 @@ def linear_workspace(desc: LinearDesc, max_tokens: int, device="cuda"):
     if n == 0:
         raise MoeError(EINVAL, "moe_linear_workspace_bytes: invalid or unsupported descriptor")
     return torch.empty(n, dtype=torch.uint8, device=device)
+
+
+def linear_path_for(desc: LinearDesc, x, T: int) -> tuple:
+    """(kernel, parts of n_in) that `linear` takes for the first T rows of x: one of LINEAR_ROWS16X8 .. TILE256X256."""
+    r = int(lib().moe_linear_path_for(ctypes.byref(desc), x.data_ptr(), _rows(x, T, desc.n_in, "x"), T))
+    if r < 0:
+        raise MoeError(r, "moe_linear_path_for")
+    return r % 256, r // 256
 
 
 def linear(desc: LinearDesc, x, T: int, out_half, out_f32, out_mode: int, ws, residual=None,

@@ -558,6 +558,7 @@ struct LinearParams {
     int vec;              // set by launch_linear: outputs and residual take four values at a time
 };
 // which kernel a product takes, and into how many parts of K it is split
+// (the numbers of moe_linear_path)
 enum LinearKind {
     kFew1, kFew2, kFew4, kTile64x32, kTile64x64, kTile128x64, kTile128x128, kAny64x32, kAny64x64, kAny128x128, kBig
 };
@@ -565,6 +566,7 @@ struct LinearPlan {
     int kind, ksplit;
 };
 size_t linear_workspace(const LinearParams &p);
+LinearPlan linear_plan(const LinearParams &p);
 void launch_linear_bf16(const LinearParams &p, const LinearPlan &c, hipStream_t st);
 void launch_linear_f16(const LinearParams &p, const LinearPlan &c, hipStream_t st);
 hipError_t launch_linear(const LinearParams &p, bool f16, hipStream_t st);

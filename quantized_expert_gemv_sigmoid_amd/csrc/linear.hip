@@ -103,11 +103,13 @@ size_t linear_workspace(const LinearParams &p)
     return ks > 1 ? std::max<size_t>(256, std::min(kPartBytes, part_bytes(p, ks))) : 256;
 }
 
+LinearPlan linear_plan(const LinearParams &p) { return plan(p, !pieces(p)); }
+
 hipError_t launch_linear(const LinearParams &params, bool f16, hipStream_t st)
 {
     LinearParams p = params;
     p.vec = fours(p);
-    const LinearPlan c = plan(p, !pieces(p));
+    const LinearPlan c = linear_plan(p);
     if (f16) launch_linear_f16(p, c, st);
     else launch_linear_bf16(p, c, st);
     return hipGetLastError();

@@ -767,6 +767,19 @@ size_t moe_linear_workspace_bytes(const moe_linear_desc *desc, int32_t max_token
     return moe::linear_workspace(linear_params(desc, max_tokens));
 }
 
+int32_t moe_linear_path_for(const moe_linear_desc *desc, const void *x, int64_t ldx, int32_t T)
+{
+    const moe_status st = check_linear(desc);
+    if (st != MOE_OK) return st;
+    if (T < 1 || ldx < desc->n_in || !x || !aligned(x, 2)) return MOE_EINVAL;
+    if (T > kMaxTokens || (T > 1 && ldx > kMaxLd)) return MOE_EUNSUPPORTED;
+    moe::LinearParams p = linear_params(desc, T);
+    p.x = x;
+    p.ldx = T == 1 ? desc->n_in : ldx;
+    const moe::LinearPlan c = moe::linear_plan(p);
+    return c.kind + 256 * c.ksplit;
+}
+
 moe_status moe_linear(const moe_linear_desc *desc, const void *x, int64_t ldx, int32_t T,
                       const void *residual, int64_t ldr, void *out_half, float *out_f32, int64_t ldo,
                       int32_t out_mode, void *ws, size_t ws_bytes, void *stream)
