@@ -62,14 +62,15 @@ __device__ __forceinline__ void tanh_parts(float x, float e, float &n, float &d)
 }
 
 // SiTU-GLU b1 tanh(g / b1) sigmoid(g) b2 tanh(u / b2) with one reciprocal for
-// the three quotients (r1 = 1 / b1, r2 = 1 / b2, b12 = b1 b2)
-__device__ __forceinline__ float situ_glu(float g, float u, float r1, float r2, float b12)
+// the three quotients (r1 = 1 / b1, r2 = 1 / b2; each beta goes to its own
+// tanh, since b1 b2 may be past fp32's range)
+__device__ __forceinline__ float situ_glu(float g, float u, float b1, float b2, float r1, float r2)
 {
     const float x = fabsf(g) * r1, y = fabsf(u) * r2;
     float n1, d1, n2, d2;
     tanh_parts(x, exp_hw(-2.0f * x), n1, d1);
     tanh_parts(y, exp_hw(-2.0f * y), n2, d2);
-    const float h = (b12 * n1) * n2 * rcp_hw(d1 * d2 * (1.0f + exp_hw(-g)));
+    const float h = (b1 * n1) * (b2 * n2) * rcp_hw(d1 * d2 * (1.0f + exp_hw(-g)));
     return __uint_as_float(__float_as_uint(h) ^ ((__float_as_uint(g) ^ __float_as_uint(u)) & 0x80000000u));
 }
 
@@ -80,7 +81,7 @@ __device__ __forceinline__ void activate(float (&a)[NV], const float (&u)[NV], i
     if (GATED) {
         if (act == MOE_LINEAR_SITU_GLU) {
 #pragma unroll
-            for (int i = 0; i < NV; i++) a[i] = situ_glu(a[i], u[i], 1.0f / b1, 1.0f / b2, b1 * b2);
+            for (int i = 0; i < NV; i++) a[i] = situ_glu(a[i], u[i], b1, b2, 1.0f / b1, 1.0f / b2);
         } else {
 #pragma unroll
             for (int i = 0; i < NV; i++) a[i] = gated_act(a[i], u[i], 1, b1, b2);
