@@ -33,9 +33,10 @@ size_t part_bytes(const LinearParams &p, int ksplit)
 }
 
 // A kernel's tile (weight rows, of both matrices where gated, by tokens); the
-// time in ns of a stage of 64 of K, base_ns + each_ns per block and CU, where
-// several blocks share a CU (otherwise the CU takes them one after the other);
-// and the rate at which it streams weights (bytes per ns).
+// time in ns of a stage of 64 of K, base_ns + each_ns per block and CU: their
+// average where several blocks share a CU, otherwise the busiest CU's, which
+// takes them one after the other; and the rate at which it streams weights
+// (bytes per ns).
 struct Kind {
     int kind, rows, tokens, base_ns, each_ns;
     bool shared, split, any;
@@ -56,13 +57,16 @@ constexpr Kind kKinds[] = {
 };
 
 // The kernel and split of K of the least estimated time: a launch, the
-// stages of the busiest CU or the weights' way from memory, and with a split
-// the partial sums' way to the join and its launch.  The constants of kKinds
-// are fits to the kernels' measured times.  Over 113 calls of M = 1 .. 4096 at
-// eight (K, N) from 515 x 333 to 7168 x 3584, timed with every kernel and
-// split, the choice is 1.8% behind the best one on average, at worst 1.4
-// times (1200 x 7168 x 896: 64 x 64 42 us, 128 x 128 in two parts 30).
-// Both sides of some: 24 x 1117 x 2049 64 x 32 in four parts 10.0 us, whole
+// stages of a CU or the weights' way from memory, and with a split the partial
+// sums' way to the join and its launch.  The constants of kKinds are fits to
+// the kernels' measured times with inputs that the caches hold.  Over 128
+// calls of M = 1 .. 4096 at ten (K, N) from 515 x 333 to 7168 x 3584, plain
+// and gated, timed with every kernel and split, the choice is 2.5% behind the
+// best one on average.  It is furthest behind where the shared kinds' blocks
+// just exceed the CUs, since their average misses the CUs that hold two: 266
+// blocks of 64 x 64 for 1200 x 7168 x 896 take 42 us (128 x 128 in two parts
+// 30), 336 for 333 x 7168 x 3584 42 us (128 x 128 in two parts 30).
+// Both sides of some others: 24 x 1117 x 2049 64 x 32 in four parts 10.0 us, whole
 // 10.2; 200 x 3584 x 7168 128 x 64 19.5, 64 x 64 21.4, 128 x 128 23.9; 800 x
 // 1117 x 2049 64 x 64 19.1, 128 x 128 19.9; 333 x 3585 x 3587 128 x 128 in two
 // parts 30.8, 64 x 64 in two 38.5; 4096 x 3584 x 7168 256 x 256 165, 128 x 128

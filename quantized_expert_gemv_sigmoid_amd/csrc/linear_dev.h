@@ -320,10 +320,11 @@ constexpr int kBigLds = 4 * kBigWave > kBigRing ? 4 * kBigWave : kBigRing;
 // 16 x 16 x 32 and not 32 x 32 x 16: on registers alone the whole chip does
 // 2050 TFLOP/s with the former and 1660-1850 with the latter, which draws
 // more power (4096 x 7168 x 7168: 372 us with the latter, 325 with the former).
-// Measured: 4096 x 7168 x 7168 296 us (1422 TFLOP/s, the library's product
-// 285-290), with bias and a 16-bit residual 315; 4096 x 3584 x 2 x 6144
-// SwiGLU 251, SiTU-GLU 273-284.  Matrix cores busy for 76% of the kernel; 8192^3
-// reaches 1491 TFLOP/s, where clocks give way to power.  The rest is the last
+// Measured: 4096 x 7168 x 7168 296-309 us by the box (1422-1360 TFLOP/s, the
+// library's product 285-293), with bias and a 16-bit residual 315-318; 4096 x
+// 3584 x 2 x 6144 SwiGLU 251-262 (library 245), SiTU-GLU 273-286.  Matrix
+// cores busy for 76% of the kernel; 8192^3 reaches 1491 TFLOP/s, where clocks
+// give way to power.  The rest is the last
 // turn of tiles (448 on 256 CUs) and the epilogue, which nothing overlaps as
 // a CU holds one block.
 template <bool F16, bool GATED>
@@ -629,15 +630,19 @@ __device__ __forceinline__ f32x4_t mfma16v(f16x8_t a, f16x8_t b, f32x4_t c)
 
 // TN weight rows (gated: TN / 2 of each matrix) x TM tokens per block, K in a
 // ring of NST stages of 64; WN x WT waves.  Each wave holds fragments a step
-// ahead of its products.  The 128 x 128 tile is bound by LDS (16 KB of
-// fragments per 2 MFLOP at 128 bytes a clock: 0.47 us a stage against 0.3 of
-// products), the small ones by a stage's latency (the ring's length beyond
+// ahead of its products.  The 128-row tiles are bound by LDS at 128 bytes a
+// clock: a stage of the 128 x 128 tile reads 96 KB of fragments (12 KB by each
+// of eight waves) and receives 32, 1024 clocks (0.47 us) against about 512 of
+// products, the 128 x 64 tile 64 and 24 KB, 704 clocks (0.32 us) against 256.
+// The small ones are bound by a stage's latency (the ring's length beyond
 // three stages changes nothing: 24 x 3584 x 6144 12.4 us with three and six).
-// Measured: 200 x 3584 x 7168 (128 x 64) 19.4 us with the weights from
-// memory (library 24), 4096 x 7168 x 896 to fp32 (128 x 128) 48 us, 53-66 with
-// x from memory (54, 64), 24 x 3584 x 2 x 6144 (64 x 32) 16.2, which is 5440
-// GB/s of weights.  Rows that are not 16-byte aligned (ANY) go through
-// registers: 333 x 1117 x 2049 14 us (library 20), 2048 x 3585 x 3587 86 (75).
+// Measured with inputs in the caches and from memory (in brackets the
+// library's product): 200 x 3584 x 7168 (128 x 64) 19.8 and 26.6 us (23, 26),
+// 4096 x 7168 x 896 to fp32 (128 x 128) 52 and 70 (56, 66), 24 x 3584 x 2 x
+// 6144 (64 x 32) 15.6 and 19.5 (21, 22), which is 4500 GB/s of weights.  Rows
+// that are not 16-byte aligned (ANY) go through registers, for both operands:
+// 333 x 1117 x 2049 12.8 and 13.9 us (21, 21), 2048 x 1117 x 2049 38 and 41
+// (27, 27), 2048 x 3585 x 3587 86 and 116 (74, 89).
 template <int TN, int TM, int WN, int WT, int NST>
 struct Tile {
     static constexpr int NW = WN * WT, THREADS = NW * 64;
@@ -919,8 +924,9 @@ __global__ __launch_bounds__(256) void k_linear_join(LinearParams p)
 // tokens; each of its eight waves takes an eighth of K through a ring of NST
 // stages of 64 in LDS of its own, filled by direct copies, so no wave waits
 // for another until the sums join.  Tokens past the end are zeros.  Bound by
-// the weights' way from memory: 1 x 7168 x 3584 10.0 us, 5140 GB/s, the rate
-// of a large copy (the first kernel, a wave per row without LDS, took 91).
+// the weights' way: 1 x 7168 x 3584 10.0 us, 5140 GB/s, where the caches hold
+// them, 11.5 us, 4470 GB/s, from memory (the first kernel, a wave per row
+// without LDS, took 91).
 // One stage more in the ring takes the same time.
 constexpr int kFewWaves = 8;
 
