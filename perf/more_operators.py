@@ -289,6 +289,12 @@ def _own(s, case):
     return {"out": s["out"], "offsets": s["offsets"], "places": s["places"]}
 
 
+def _scaled(x, e):
+    """x 2^e, the powers made from their bits (pow may be off by a bit), in two steps that hold any exponent."""
+    h = e.int() >> 1
+    return x * ((h + 127) << 23).view(torch.float32) * ((e.int() - h + 127) << 23).view(torch.float32)
+
+
 def _blocks(x, rule):
     """E2M1 numbers of rows x [T][K] in blocks [T][K / 32][32], and the exponents of their scales."""
     b = x.reshape(x.shape[0], -1, 32)
@@ -298,7 +304,7 @@ def _blocks(x, rule):
     if rule == "fit":
         e = e + (m > 0.75).int()
     e = torch.where(top > 0, e, -127).clamp_min(-127)
-    v = torch.ldexp(b, -e)
+    v = _scaled(b, -e)
     a = v.abs()
     step = torch.where(a < 2, 0.5, torch.where(a < 4, 1.0, 2.0))
     return torch.copysign((torch.round(a / step) * step).clamp_max(6.0), v), e
@@ -309,14 +315,14 @@ def _plain_quant(s, case):
     x = torch.zeros(T, (K + 31) // 32 * 32, device=s["x"].device)
     x[:, :K] = s["x"].float()
     n, e = _blocks(x, case["rule"])
-    return torch.ldexp(n, e).view(T, -1)[:, :K].to(_TYPES[case["type"]])
+    return _scaled(n, e).view(T, -1)[:, :K].to(_TYPES[case["type"]])
 
 
 def _values(codes, scales):
     """The fp32 values of MXFP4 rows."""
     table = torch.tensor(_E2M1 + tuple(-v for v in _E2M1), device=codes.device)
     n = table[torch.stack([codes & 15, codes >> 4], -1).long()].view(*scales.shape, 32)
-    return torch.ldexp(n, scales[..., None].int() - 127).view(*codes.shape[:-1], -1)
+    return _scaled(n, scales[..., None].int() - 127).view(*codes.shape[:-1], -1)
 
 
 def _act(act, a, u):
@@ -412,9 +418,9 @@ def _exact_quant(s, case):
         x = s["x"][a:a + step].double()
         b = torch.nn.functional.pad(x, (0, blocks * 32 - K)).view(-1, blocks, 32)
         top = b.abs().max(2).values
-        # 2^(e + 2), the power of two at or below the largest magnitude
-        power = torch.where(top > 0, torch.exp2(torch.floor(torch.log2(torch.where(top > 0, top, 1.0)))), 0.0)
-        power = torch.where(power > top, power / 2, torch.where(2 * power <= top, 2 * power, power))
+        # the power of two at or below the largest magnitude: that over its fraction in [1, 2)
+        fraction = 2 * torch.frexp(top).mantissa
+        power = torch.where(top > 0, top / torch.where(top > 0, fraction, 1.0), 0.0)
         scale = power / 4
         if case["rule"] == "fit":
             scale = torch.where(top > 6 * scale, 2 * scale, scale)
@@ -435,7 +441,8 @@ def _values64(codes, scales):
     e, m, neg = (c >> 1) & 3, (c & 1).double(), c > 7
     v = torch.where(e == 0, m / 2, (1 + m / 2) * torch.exp2((e - 1).double()))
     v = torch.where(neg, -v, v)
-    return v * torch.exp2(scales.double() - 127).repeat_interleave(32, dim=-1)
+    power = ((scales.long() + (1023 - 127)) << 52).view(torch.float64)
+    return v * power.repeat_interleave(32, dim=-1)
 
 
 def _act64(act, a, u):
