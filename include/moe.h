@@ -323,7 +323,8 @@ moe_status moe_latent_layer_timed(const moe_latent_desc *desc, const uint16_t *x
  * score of its token); a NaN c ranks with +inf, so it is chosen and its NaN
  * weight shows.
  */
-typedef enum { MOE_BF16 = 0, MOE_F16 = 1, MOE_F32 = 2 } moe_type;
+/* (MOE_MXFP4: operands of moe_grouped_linear only) */
+typedef enum { MOE_BF16 = 0, MOE_F16 = 1, MOE_F32 = 2, MOE_MXFP4 = 3 } moe_type;
 typedef enum { MOE_SCORE_SIGMOID = 0, MOE_SCORE_SOFTMAX = 1 } moe_score;
 typedef enum { MOE_GROUP_MAX = 0, MOE_GROUP_TOP2 = 1 } moe_group_score;
 
@@ -432,6 +433,154 @@ int32_t moe_linear_path_for(const moe_linear_desc *desc, const void *x, int64_t 
 moe_status moe_linear(const moe_linear_desc *desc, const void *x, int64_t ldx, int32_t T,
                       const void *residual, int64_t ldr, void *out_half, float *out_f32,
                       int64_t ldo, int32_t out_mode, void *ws, size_t ws_bytes, void *stream);
+
+/*
+ * MXFP4 rows: codes and scales as moe_layer_desc's (the low nibble first, one
+ * E8M0 byte per 32 values of a row), made and read back.
+ *
+ *   block of 32 values, the last one of a row filled up with zeros:
+ *   e = floor(log2(largest magnitude)) - 2      (MOE_MX_FLOOR, the format's own
+ *                                                rule: magnitudes past 6 * 2^e
+ *                                                become 6 * 2^e), or
+ *   e = the least with largest magnitude <= 6 * 2^e                (MOE_MX_FIT),
+ *   and at least -127 in both; scale byte e + 127;
+ *   code = value / 2^e as E2M1 (0, 0.5, 1, 1.5, 2, 3, 4, 6 and a sign), round
+ *   to nearest, ties to the even code.
+ *
+ * A block without a value but zeros has scale byte 0.  One with an infinity
+ * or a NaN has byte 255 and codes of 0: moe_mx_dequantize reads NaN for its
+ * values, a product with them is NaN (and a layer, as moe_layer_desc says,
+ * drops the block).  Reading back is exact but for fp32 outputs' overflow to
+ * infinity and fp16's rounding, range and subnormals.
+ */
+typedef enum { MOE_MX_FLOOR = 0, MOE_MX_FIT = 1 } moe_mx_rule;
+
+/*
+ * x: T rows of n values of `type` (moe_type), ldx elements apart.  codes: rows
+ * of 16 ceil(n / 32) bytes, ldc bytes apart; scales: rows of ceil(n / 32)
+ * bytes, lds bytes apart; bytes between rows stay as they are.  Elements need
+ * their own alignment only.  1 <= n <= 2^20.  Weights of several experts are
+ * rows one after the other.
+ */
+moe_status moe_mx_quantize(const void *x, int32_t type, int64_t ldx, int32_t T, int32_t n, int32_t rule, uint8_t *codes,
+                           int64_t ldc, uint8_t *scales, int64_t lds, void *stream);
+
+/* The values of such rows: out, T rows of n values of `type`, ldo elements apart. */
+moe_status moe_mx_dequantize(const uint8_t *codes, int64_t ldc, const uint8_t *scales, int64_t lds, int32_t T, int32_t n, void *out,
+                             int32_t type, int64_t ldo, void *stream);
+
+/*
+ * moe_linear on MXFP4 rows x, w, w_up: the same formula, activations, biases,
+ * residual and outputs.  A product of 128 codes of a row is summed as the
+ * matrix cores do, terms below about 2^-24 of its largest one cut off; the
+ * rest as moe_linear.  Scale byte 255 is NaN (0 in the layer).
+ *
+ * n_in is a multiple of 32 (moe_mx_quantize fills up other rows: n_in is then
+ * the next one).  Rows of codes start at multiples of 16 bytes, scales
+ * anywhere; where n_in is no multiple of 128 or scale rows do not start at
+ * multiples of 4 bytes, a launch before the product copies them into the
+ * workspace.
+ */
+typedef struct {
+    int32_t n_in, n_out;
+    int32_t type;            /* moe_type of the 16-bit output: MOE_BF16, MOE_F16  */
+    int32_t act;             /* moe_linear_act                                   */
+    float situ_b1, situ_b2;  /* SiTU betas; unused otherwise                      */
+    int32_t bias_type;       /* MOE_F32 or `type`                                */
+    int32_t residual_type;   /* MOE_F32 or `type`                                */
+    int64_t ldw, ldw_s;      /* bytes between rows of codes, of scales            */
+    const uint8_t *w, *w_up;     /* [n_out][n_in / 2]; w_up: gated activations    */
+    const uint8_t *w_s, *w_up_s; /* [n_out][n_in / 32]                           */
+    const void *bias, *bias_up;  /* as moe_linear_desc                           */
+} moe_mx_linear_desc;
+
+/* As moe_linear's.  The kernels are moe_linear's too (moe_linear_path; never
+ * one of ANY). */
+size_t moe_mx_linear_workspace_bytes(const moe_mx_linear_desc *desc, int32_t max_tokens);
+int32_t moe_mx_linear_path_for(const moe_mx_linear_desc *desc, int32_t T);
+
+/* x, x_s: T rows of codes and of scales, ldx and ldxs bytes apart (up to 2^23
+ * and 2^22); the rest as moe_linear. */
+moe_status moe_mx_linear(const moe_mx_linear_desc *desc, const uint8_t *x, int64_t ldx, const uint8_t *x_s, int64_t ldxs, int32_t T,
+                         const void *residual, int64_t ldr, void *out_half, float *out_f32, int64_t ldo, int32_t out_mode,
+                         void *ws, size_t ws_bytes, void *stream);
+
+/*
+ * Experts of other precisions than the layer's, one product at a time: the
+ * choices of a routing sorted by expert (moe_group), the products of each
+ * expert's rows with its weights (moe_grouped_linear), and the rows of each
+ * token added up (moe_combine).
+ *
+ * moe_group: ids [T][k] as moe_gate writes them (an id outside [0, n_experts)
+ * is no choice; the same id may come again in a row).  Rows, one per choice,
+ * are sorted by expert and inside one by (token, choice):
+ *   offsets[n_experts + 1]: expert e's are offsets[e] .. offsets[e + 1] - 1;
+ *   tokens[T k]: the token of each row (the places from offsets[n_experts] on
+ *   are left as they are);
+ *   places[T][k]: the row of each choice, -1 for none.
+ * n_experts up to 1024, k up to 64.  Workspace as moe_linear's.
+ */
+size_t moe_group_workspace_bytes(int32_t max_tokens, int32_t top_k, int32_t n_experts);
+moe_status moe_group(const int32_t *ids, int32_t T, int32_t top_k, int32_t n_experts, int32_t *offsets, int32_t *tokens,
+                     int32_t *places, void *ws, size_t ws_bytes, void *stream);
+
+/*
+ * out[r] = act(sum_k x[rows[r]][k] w[g][n][k] + bias[g][n] (, the same of w_up))
+ * for the rows r of group g, offsets[g] <= r < offsets[g + 1]; activations and
+ * sums as moe_linear's (MXFP4: as moe_mx_linear's).
+ */
+typedef struct {
+    int32_t n_groups, n_in, n_out;   /* up to 1024, 2^20, 2^20                    */
+    int32_t type;            /* MOE_BF16 or MOE_F16: 16-bit operands and output   */
+    int32_t operands;        /* moe_type of x, w, w_up: `type` or MOE_MXFP4       */
+    int32_t act;             /* moe_linear_act                                   */
+    float situ_b1, situ_b2;  /* SiTU betas; unused otherwise                      */
+    int32_t bias_type;       /* MOE_F32 or `type`                                */
+    int64_t ldw, group_w;    /* elements (MXFP4: bytes) between rows of w and w_up,
+                                and between groups' matrices (>= 0)               */
+    int64_t ldw_s, group_w_s;/* MXFP4: bytes between rows of scales, and groups'  */
+    const void *w, *w_up;    /* [n_groups][n_out][n_in]                          */
+    const uint8_t *w_s, *w_up_s; /* MXFP4: [n_groups][n_out][n_in / 32]          */
+    const void *bias, *bias_up;  /* [n_groups][n_out], or NULL                   */
+} moe_grouped_desc;
+
+/* The kernel that moe_grouped_linear takes for R >= 1 rows: a moe_linear_path
+ * + 256. */
+int32_t moe_grouped_path_for(const moe_grouped_desc *desc, const void *x, int64_t ldx, int32_t R);
+
+/*
+ * x: x_rows rows of n_in values, ldx elements (MXFP4: bytes; x_s, ldxs the
+ * scales' rows; both NULL / unused otherwise) apart.  rows: [R] the row of x
+ * behind each row, a row of zeros for one outside [0, x_rows); or NULL: row r
+ * is x's own (x_rows >= R).  offsets: [n_groups + 1], not decreasing; rows
+ * before offsets[0] and from min(offsets[n_groups], R) on are left as they
+ * are.  Offsets outside [0, R] count as its ends.  rows and offsets are read on
+ * the device, so the call needs no synchronisation behind moe_group.
+ *
+ * 0 <= R <= 2^24; ldx, ldw, ldo up to 2^22 (MXFP4: ldx, ldw up to 2^23, ldxs,
+ * ldw_s to 2^22); with `rows`, x's rows lie within 2 GiB.  MXFP4: n_in a multiple
+ * of 128, rows of codes at multiples of 16 bytes, rows of scales at multiples
+ * of 4 (MOE_EUNSUPPORTED for n_in and the scales).  16-bit elements need their
+ * own alignment only; rows at multiples of 16 bytes, n_in of 8, take the
+ * faster kernels.  Outputs as moe_linear's; they must not overlap inputs.
+ * Needs no workspace.
+ */
+moe_status moe_grouped_linear(const moe_grouped_desc *desc, const void *x, int64_t ldx, const uint8_t *x_s, int64_t ldxs,
+                              int32_t x_rows, const int32_t *rows, const int32_t *offsets, int32_t R, void *out_half,
+                              float *out_f32, int64_t ldo, int32_t out_mode, void *stream);
+
+/*
+ * out[t][i] = sum_j weights[t][j] y[places[t][j]][i] + residual[t][i], j in its
+ * order, in fp32, rounded once.  y: R rows of n values, ldy elements apart; a
+ * place outside [0, R) adds nothing.  weights: [T][k] fp32, or NULL for 1.
+ * residual: NULL, or T rows ldr apart (0: the same row for every token).
+ * y, residual and out (rows ldo apart) each have a moe_type of their own
+ * (MOE_BF16, MOE_F16, MOE_F32).  out may be the residual's own buffer (same
+ * pointer, row distance and type).  k up to 64, n up to 2^20.
+ */
+moe_status moe_combine(const void *y, int32_t y_type, int64_t ldy, int32_t R, const int32_t *places, const float *weights, int32_t T,
+                       int32_t top_k, int32_t n, const void *residual, int32_t residual_type, int64_t ldr, void *out,
+                       int32_t out_type, int64_t ldo, void *stream);
 
 /* Static text for a status code. */
 const char *moe_status_str(int32_t status);

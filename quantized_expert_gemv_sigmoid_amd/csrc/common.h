@@ -556,7 +556,28 @@ struct LinearParams {
     int64_t ldo;
     float *part;          // workspace
     int vec;              // set by launch_linear: outputs and residual take four values at a time
+    static constexpr bool grouped = false, mx = false;
 };
+// Rows in groups, each with weights of its own (moe_grouped_linear): M counts
+// the rows of all groups, w, w_up and the biases are those of group 0.
+struct GroupedParams : LinearParams {
+    const int32_t *offsets;    // [groups + 1]
+    const int32_t *rows;       // the row of x behind each row, or null: its own
+    int groups, xrows;         // xrows: rows of x
+    int64_t wstride, bstride;  // elements between groups' weights, biases
+    static constexpr bool grouped = true;
+};
+// MXFP4 operands: K, ldx, ldw (and wstride) count 16-bit units, four codes
+// each, so that a row is as long as a 16-bit row of a quarter of its values;
+// scale rows start at multiples of four bytes and hold multiples of four.
+template <class Base>
+struct MxOf : Base {
+    const uint8_t *xs, *ws, *us;  // scales of x, w, w_up
+    int64_t ldxs, ldws, sstride;  // bytes between rows; between groups' scales
+    static constexpr bool mx = true;
+};
+using MxParams = MxOf<LinearParams>;
+using GroupedMxParams = MxOf<GroupedParams>;
 // which kernel a product takes, and into how many parts of K it is split
 // (the numbers of moe_linear_path)
 enum LinearKind {
@@ -570,5 +591,44 @@ LinearPlan linear_plan(const LinearParams &p);
 void launch_linear_bf16(const LinearParams &p, const LinearPlan &c, hipStream_t st);
 void launch_linear_f16(const LinearParams &p, const LinearPlan &c, hipStream_t st);
 hipError_t launch_linear(const LinearParams &p, bool f16, hipStream_t st);
+
+// ---- MXFP4 rows, their product, products of groups, the groups themselves
+
+hipError_t launch_mx_quantize(const void *x, int type, int64_t ldx, int64_t rows, int cols, uint8_t *codes, int64_t ldc,
+                              uint8_t *scales, int64_t lds, int fit, hipStream_t st);
+hipError_t launch_mx_dequantize(const uint8_t *codes, int64_t ldc, const uint8_t *scales, int64_t lds, int64_t rows, int cols,
+                                void *out, int type, int64_t ldo, hipStream_t st);
+// rows of `blocks` scales of w, w_up (or null) and x into rows of `pitch` bytes
+hipError_t launch_mx_scale_rows(const uint8_t *w, const uint8_t *w_up, int64_t ldw, int n, const uint8_t *x, int64_t ldx, int t,
+                                int blocks, int pitch, uint8_t *out, hipStream_t st);
+
+size_t mx_linear_workspace(const MxParams &p);
+LinearPlan mx_linear_plan(const MxParams &p);
+void launch_mx_bf16(const MxParams &p, const LinearPlan &c, hipStream_t st);
+void launch_mx_f16(const MxParams &p, const LinearPlan &c, hipStream_t st);
+hipError_t launch_mx_linear(const MxParams &p, bool f16, hipStream_t st);
+
+LinearPlan grouped_plan(const GroupedParams &p, bool mx);
+void launch_grouped_bf16(const GroupedParams &p, const LinearPlan &c, hipStream_t st);
+void launch_grouped_f16(const GroupedParams &p, const LinearPlan &c, hipStream_t st);
+void launch_grouped_mx_bf16(const GroupedMxParams &p, const LinearPlan &c, hipStream_t st);
+void launch_grouped_mx_f16(const GroupedMxParams &p, const LinearPlan &c, hipStream_t st);
+hipError_t launch_grouped(const GroupedParams &p, bool f16, hipStream_t st);
+hipError_t launch_grouped_mx(const GroupedMxParams &p, bool f16, hipStream_t st);
+
+size_t group_workspace(int64_t R, int E);
+hipError_t launch_group(const int32_t *ids, int64_t R, int k, int E, int32_t *offsets, int32_t *tokens, int32_t *places,
+                        void *ws, hipStream_t st);
+
+struct CombineParams {
+    const void *y, *res;
+    const int32_t *places;
+    const float *weights;  // or null: 1
+    void *out;
+    int64_t ldy, ldr, ldo;
+    int T, k, n, rows, t0;
+    int res_type, out_type;
+};
+hipError_t launch_group_combine(const CombineParams &p, int y_type, hipStream_t st);
 
 }  // namespace moe

@@ -1,0 +1,250 @@
+// The choices of tokens sorted by expert (moe_group), and the experts' rows
+// added up again (moe_combine).
+#include <algorithm>
+
+#include "../../include/moe.h"
+#include "common.h"
+
+namespace moe {
+
+namespace {
+
+// A counting sort that keeps the order of the choices inside an expert, so the
+// same call always gives the same places.  Each wave owns a run of choices and
+// goes through it 64 at a time; a choice's rank among the wave's is what the
+// wave has counted of its expert so far plus the lower lanes that chose it too.
+constexpr int kGroupWaves = 16;
+constexpr int kGroupThreads = kGroupWaves * 64;
+
+// lanes whose id equals this lane's, for ids below 2^10, kNone among them
+__device__ __forceinline__ uint64_t same_lanes(int id, bool on)
+{
+    uint64_t m = __ballot(on);
+#pragma unroll
+    for (int b = 0; b < 10; b++) {
+        const uint64_t v = __ballot((id >> b) & 1);
+        m &= (id >> b) & 1 ? v : ~v;
+    }
+    return m;
+}
+
+// counts[w][e] of the block's waves, over choices [a, b) of the block
+__device__ __forceinline__ void count_choices(const int32_t *ids, int64_t a, int64_t b, int E, int *counts)
+{
+    const int lane = threadIdx.x & 63, wv = threadIdx.x >> 6;
+    const int64_t per = (b - a + kGroupWaves - 1) / kGroupWaves, a0 = a + wv * per, b0 = min(b, a0 + per);
+    int *mine = counts + wv * E;
+    for (int64_t i = a0; i < b0; i += 64) {
+        const int id = i + lane < b0 ? ids[i + lane] : -1;
+        const bool on = (uint32_t)id < (uint32_t)E;
+        const uint64_t same = same_lanes(id, on);
+        if (on && (same & ((1ull << lane) - 1)) == 0) mine[id] += __popcll(same);  // (one lane per expert)
+    }
+}
+
+// Grid: blocks of `per` choices each.  One block does all; of several, a first
+// launch writes their counts to hist [blocks][E].
+__global__ __launch_bounds__(kGroupThreads) void k_group_count(const int32_t *ids, int64_t R, int64_t per, int E, int32_t *hist)
+{
+    __shared__ int lds_i[kGroupWaves * kMaxExperts];
+    for (int i = threadIdx.x; i < kGroupWaves * E; i += kGroupThreads) lds_i[i] = 0;
+    __syncthreads();
+    const int64_t a = blockIdx.x * per;
+    count_choices(ids, a, min(R, a + per), E, lds_i);
+    __syncthreads();
+    for (int e = threadIdx.x; e < E; e += kGroupThreads) {
+        int s = 0;
+        for (int w = 0; w < kGroupWaves; w++) s += lds_i[w * E + e];
+        hist[blockIdx.x * E + e] = s;
+    }
+}
+
+__global__ __launch_bounds__(kGroupThreads) void k_group_place(const int32_t *ids, int64_t R, int64_t per, int k, int E,
+                                                               const int32_t *hist, int32_t *offsets, int32_t *tokens,
+                                                               int32_t *places)
+{
+    __shared__ int lds_i[kGroupWaves * kMaxExperts], sums[kGroupWaves];
+    const int lane = threadIdx.x & 63, wv = threadIdx.x >> 6;
+    for (int i = threadIdx.x; i < kGroupWaves * E; i += kGroupThreads) lds_i[i] = 0;
+    __syncthreads();
+    const int64_t a = blockIdx.x * per, b = min(R, a + per);
+    count_choices(ids, a, b, E, lds_i);
+    __syncthreads();
+    // thread e: the choices of expert e in the blocks before this one, in all,
+    // and before each of its waves
+    const int e = threadIdx.x;
+    int before = 0, total = 0;
+    if (e < E) {
+        for (int w = 0; w < kGroupWaves; w++) {
+            const int c = lds_i[w * E + e];
+            lds_i[w * E + e] = total;
+            total += c;
+        }
+        if (gridDim.x > 1) {
+            total = 0;
+            for (int g = 0; g < (int)gridDim.x; g++) {
+                const int c = hist[g * E + e];
+                if (g < (int)blockIdx.x) before += c;
+                total += c;
+            }
+        }
+    }
+    int scan = total;  // over the experts
+#pragma unroll
+    for (int d = 1; d < 64; d <<= 1) {
+        const int v = __shfl_up(scan, d, 64);
+        if (lane >= d) scan += v;
+    }
+    if (lane == 63) sums[wv] = scan;
+    __syncthreads();
+    int base = scan - total;
+    for (int w = 0; w < wv; w++) base += sums[w];
+    if (e < E) {
+        for (int w = 0; w < kGroupWaves; w++) lds_i[w * E + e] += base + before;
+        if (blockIdx.x == 0) {
+            offsets[e] = base;
+            if (e == E - 1) offsets[E] = base + total;
+        }
+    }
+    __syncthreads();
+    const int64_t run = (b - a + kGroupWaves - 1) / kGroupWaves, a0 = a + wv * run, b0 = min(b, a0 + run);
+    int *mine = lds_i + wv * E;
+    for (int64_t i = a0; i < b0; i += 64) {
+        const int64_t c = i + lane;
+        const int id = c < b0 ? ids[c] : -1;
+        const bool on = (uint32_t)id < (uint32_t)E;
+        const uint64_t same = same_lanes(id, on), lower = same & ((1ull << lane) - 1);
+        int place = -1;
+        if (on) {
+            const int first = mine[id];
+            place = first + __popcll(lower);
+            if (lower == 0) mine[id] = first + __popcll(same);
+            tokens[place] = (int32_t)(c / k);
+        }
+        if (c < b0) places[c] = place;
+    }
+}
+
+// --------------------------------------------------------------- combination
+
+// eight values of a row in fp32
+__device__ __forceinline__ void read8(const void *p, int type, int64_t at, int n, float (&v)[8])
+{
+    if (type == MOE_F32) {
+        const float *f = reinterpret_cast<const float *>(p) + at;
+        if (n >= 8) {
+            __builtin_memcpy(v, f, 32);
+        } else {
+#pragma unroll
+            for (int j = 0; j < 8; j++) v[j] = j < n ? f[j] : 0.0f;
+        }
+        return;
+    }
+    const uint16_t *h = reinterpret_cast<const uint16_t *>(p) + at;
+    uint16_t q[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+    if (n >= 8) {
+        __builtin_memcpy(q, h, 16);
+    } else {
+#pragma unroll
+        for (int j = 0; j < 8; j++)
+            if (j < n) q[j] = h[j];
+    }
+#pragma unroll
+    for (int j = 0; j < 8; j++)
+        v[j] = type == MOE_F16 ? (float)__builtin_bit_cast(_Float16, q[j]) : __uint_as_float((uint32_t)q[j] << 16);
+}
+
+// A thread adds eight columns of a token's rows, in the order of its choices,
+// fp32 throughout; YT: the rows' type.
+template <int YT>
+__global__ __launch_bounds__(256) void k_group_combine(CombineParams p)
+{
+    const int t = blockIdx.y + p.t0, n0 = (blockIdx.x * 256 + threadIdx.x) * 8;
+    if (n0 >= p.n) return;
+    const int n = min(8, p.n - n0);
+    const int32_t *pl = p.places + (int64_t)t * p.k;
+    const float *wt = p.weights ? p.weights + (int64_t)t * p.k : nullptr;
+    float s[8] = {};
+    constexpr int B = 4;
+    for (int j0 = 0; j0 < p.k; j0 += B) {
+        float v[B][8], w[B];
+#pragma unroll
+        for (int j = 0; j < B; j++) {
+            const int place = j0 + j < p.k ? pl[j0 + j] : -1;
+            const bool on = (uint32_t)place < (uint32_t)p.rows;
+            w[j] = on ? (wt ? wt[j0 + j] : 1.0f) : 0.0f;
+            if (on) {
+                read8(p.y, YT, (int64_t)place * p.ldy + n0, n, v[j]);
+            } else {
+#pragma unroll
+                for (int i = 0; i < 8; i++) v[j][i] = 0.0f;
+            }
+        }
+#pragma unroll
+        for (int j = 0; j < B; j++)
+#pragma unroll
+            for (int i = 0; i < 8; i++) s[i] = fmaf(w[j], v[j][i], s[i]);
+    }
+    if (p.res) {
+        float r[8];
+        read8(p.res, p.res_type, (int64_t)t * p.ldr + n0, n, r);
+#pragma unroll
+        for (int i = 0; i < 8; i++) s[i] += r[i];
+    }
+    const int64_t at = (int64_t)t * p.ldo + n0;
+    if (p.out_type == MOE_F32) {
+        float *o = reinterpret_cast<float *>(p.out) + at;
+        if (n == 8) {
+            __builtin_memcpy(o, s, 32);
+        } else {
+#pragma unroll
+            for (int i = 0; i < 8; i++)
+                if (i < n) o[i] = s[i];
+        }
+        return;
+    }
+    uint16_t h[8], *o = reinterpret_cast<uint16_t *>(p.out) + at;
+#pragma unroll
+    for (int i = 0; i < 8; i++)
+        h[i] = p.out_type == MOE_F16 ? __builtin_bit_cast(uint16_t, (_Float16)s[i]) : f32_to_bf16_rne(s[i]);
+    if (n == 8) {
+        __builtin_memcpy(o, h, 16);
+    } else {
+#pragma unroll
+        for (int i = 0; i < 8; i++)
+            if (i < n) o[i] = h[i];
+    }
+}
+
+// choices of a block and the blocks of a call
+int64_t group_per(int64_t R) { return std::max<int64_t>(4096, (R + 63) / 64); }
+
+}  // namespace
+
+size_t group_workspace(int64_t R, int E) { return R > group_per(R) ? (size_t)((R + group_per(R) - 1) / group_per(R)) * E * 4 : 256; }
+
+hipError_t launch_group(const int32_t *ids, int64_t R, int k, int E, int32_t *offsets, int32_t *tokens, int32_t *places,
+                        void *ws, hipStream_t st)
+{
+    const int64_t per = group_per(R);
+    const int blocks = (int)std::max<int64_t>(1, (R + per - 1) / per);
+    int32_t *hist = reinterpret_cast<int32_t *>(ws);
+    if (blocks > 1) k_group_count<<<blocks, kGroupThreads, 0, st>>>(ids, R, per, E, hist);
+    k_group_place<<<blocks, kGroupThreads, 0, st>>>(ids, R, per, k, E, hist, offsets, tokens, places);
+    return hipGetLastError();
+}
+
+hipError_t launch_group_combine(const CombineParams &params, int y_type, hipStream_t st)
+{
+    CombineParams p = params;
+    const int total = p.T;
+    for (p.t0 = 0; p.t0 < total; p.t0 += 65535) {
+        const dim3 grid((p.n + 2047) / 2048, std::min(65535, total - p.t0));
+        if (y_type == MOE_F32) k_group_combine<MOE_F32><<<grid, 256, 0, st>>>(p);
+        else if (y_type == MOE_F16) k_group_combine<MOE_F16><<<grid, 256, 0, st>>>(p);
+        else k_group_combine<MOE_BF16><<<grid, 256, 0, st>>>(p);
+    }
+    return hipGetLastError();
+}
+
+}  // namespace moe

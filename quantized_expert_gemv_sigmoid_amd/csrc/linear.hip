@@ -1,4 +1,5 @@
-// moe_linear's choice of kernel (linear_dev.h), and its workspace.
+// The choice of kernel (linear_dev.h) of moe_linear, moe_mx_linear and
+// moe_grouped_linear, and their workspaces.
 #include <algorithm>
 #include <cmath>
 
@@ -108,6 +109,108 @@ size_t linear_workspace(const LinearParams &p)
 }
 
 LinearPlan linear_plan(const LinearParams &p) { return plan(p, !pieces(p)); }
+
+// ------------------------------------------------------------ MXFP4 operands
+
+namespace {
+
+int scale_pitch(const LinearParams &p) { return (p.K + 63) / 64 * 8; }  // 8 scales a stage
+// the kernels copy scales as dwords
+bool dwords(const LinearParams &p, const uint8_t *a, const uint8_t *b, int64_t ld, int rows)
+{
+    return p.K % 32 == 0 && (((uintptr_t)a | (uintptr_t)b) & 3) == 0 && (rows == 1 || ld % 4 == 0);
+}
+size_t up256(size_t n) { return (n + 255) & ~(size_t)255; }
+// rows of weight scales that the workspace has a copy of, and room for x's
+size_t weight_scales(const MxParams &p)
+{
+    return dwords(p, p.ws, p.us, p.ldws, p.N) ? 0 : up256((size_t)(p.us ? 2 : 1) * p.N * scale_pitch(p));
+}
+size_t x_scales(const MxParams &p) { return up256((size_t)p.M * scale_pitch(p)); }
+
+}  // namespace
+
+size_t mx_linear_workspace(const MxParams &p) { return up256(linear_workspace(p)) + weight_scales(p) + x_scales(p); }
+
+// A stage of 256 codes takes the bytes, reads and cycles of a 16-bit one of 64
+LinearPlan mx_linear_plan(const MxParams &p) { return plan(p, false); }
+
+hipError_t launch_mx_linear(const MxParams &params, bool f16, hipStream_t st)
+{
+    MxParams p = params;
+    p.vec = fours(p);
+    const bool wd = dwords(p, p.ws, p.us, p.ldws, p.N), xd = dwords(p, p.xs, nullptr, p.ldxs, p.M);
+    if (!wd || !xd) {
+        const int pitch = scale_pitch(p);
+        uint8_t *at = reinterpret_cast<uint8_t *>(p.part) + up256(linear_workspace(p));
+        const size_t wrows = wd ? 0 : (size_t)(p.us ? 2 : 1) * p.N;
+        const hipError_t e = launch_mx_scale_rows(p.ws, wd ? nullptr : p.us, p.ldws, wd ? 0 : p.N, p.xs, p.ldxs, xd ? 0 : p.M, p.K / 8,
+                                                  pitch, at, st);
+        if (e != hipSuccess) return e;
+        if (!wd) {
+            p.ws = at;
+            if (p.us) p.us = at + (size_t)p.N * pitch;
+            p.ldws = pitch;
+        }
+        if (!xd) {
+            p.xs = at + wrows * pitch;
+            p.ldxs = pitch;
+        }
+    }
+    const LinearPlan c = mx_linear_plan(p);
+    if (f16) launch_mx_f16(p, c, st);
+    else launch_mx_bf16(p, c, st);
+    return hipGetLastError();
+}
+
+// -------------------------------------------------------------------- groups
+
+// plan()'s estimate where the rows of each group are not known: as if the M
+// rows fell on the groups at random, which leaves some of them empty where
+// there are few rows, and a tile of each other group half full on average.
+LinearPlan grouped_plan(const GroupedParams &p, bool mx)
+{
+    const bool any = !mx && !(pieces(p) && p.wstride % 8 == 0);
+    const int m = p.w_up ? 2 : 1, stages = (p.K + 63) / 64;
+    const double active = p.groups * (1.0 - std::exp(-(double)p.M / p.groups));
+    const double weights = 2.0 * m * active * p.N * p.K;
+    LinearPlan best = {any ? kAny128x128 : kBig, 1};
+    double least = 1e30;
+    for (const Kind &k : kKinds) {
+        if (k.any != any) continue;
+        const double columns = std::ceil((double)p.N * m / k.rows);
+        if (columns * ((double)p.M / k.tokens + p.groups) > 1e9) continue;
+        const double tiles = columns * std::max(active, (double)p.M / k.tokens + 0.5 * active);
+        const double full = tiles / kCus, each = k.shared ? std::max(1.0, full) : std::ceil(full);
+        const double work = (k.base_ns + each * k.each_ns) * stages;
+        const double ns = std::max(work, weights / k.rate) + 0.1 * work;
+        if (ns < least) {
+            least = ns;
+            best = {k.kind, 1};
+        }
+    }
+    return best;
+}
+
+hipError_t launch_grouped(const GroupedParams &params, bool f16, hipStream_t st)
+{
+    GroupedParams p = params;
+    p.vec = fours(p);
+    const LinearPlan c = grouped_plan(p, false);
+    if (f16) launch_grouped_f16(p, c, st);
+    else launch_grouped_bf16(p, c, st);
+    return hipGetLastError();
+}
+
+hipError_t launch_grouped_mx(const GroupedMxParams &params, bool f16, hipStream_t st)
+{
+    GroupedMxParams p = params;
+    p.vec = fours(p);
+    const LinearPlan c = grouped_plan(p, true);
+    if (f16) launch_grouped_mx_f16(p, c, st);
+    else launch_grouped_mx_bf16(p, c, st);
+    return hipGetLastError();
+}
 
 hipError_t launch_linear(const LinearParams &params, bool f16, hipStream_t st)
 {

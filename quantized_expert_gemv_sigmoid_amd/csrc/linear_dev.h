@@ -16,6 +16,8 @@
 #pragma once
 
 #include <math.h>
+
+#include <algorithm>
 #include <type_traits>
 
 #include "../../include/moe.h"
@@ -297,8 +299,15 @@ __device__ __forceinline__ __amdgpu_buffer_rsrc_t rows_rsrc(const uint16_t *base
     return grsrc(base, bytes);
 }
 
-// 16 bytes per lane at voff of r to LDS at dst + 16 lane (dst wave-uniform).
+// 16 (4) bytes per lane at voff of r to LDS at dst + 16 (4) lane (dst wave-uniform).
 // The caller orders the copies with waits and barriers.
+__device__ __forceinline__ void copy4(__amdgpu_buffer_rsrc_t r, uint32_t dst, uint32_t voff)
+{
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dword %1, %2, 0 offen lds"
+                 :
+                 : "s"(__builtin_amdgcn_readfirstlane(dst)), "v"(voff), "s"(r)
+                 : "memory", "m0");
+}
 __device__ __forceinline__ void copy16(__amdgpu_buffer_rsrc_t r, uint32_t dst, uint32_t voff)
 {
     asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds"
@@ -313,169 +322,110 @@ constexpr int kBigRow = 64 * 4 + 16;        // a row of the epilogue's buffer
 constexpr int kBigWave = 128 * kBigRow;  // a wave's part of it
 constexpr int kBigLds = 4 * kBigWave > kBigRing ? 4 * kBigWave : kBigRing;
 
-// 256 x 256 outputs (gated: 128 of each matrix) per block and CU, four waves
-// of 128 x 128, one to a SIMD, whose 256 sums per lane fill the accumulation
-// registers: 64 products of 16 x 16 x 32 per 32 fragment reads of 16 bytes,
-// so LDS supplies half of what it could, and the matrix cores are the bound.
-// 16 x 16 x 32 and not 32 x 32 x 16: on registers alone the whole chip does
-// 2050 TFLOP/s with the former and 1660-1850 with the latter, which draws
-// more power (4096 x 7168 x 7168: 372 us with the latter, 325 with the former).
-// Measured: 4096 x 7168 x 7168 296-309 us by the box (1422-1360 TFLOP/s, the
-// library's product 285-293), with bias and a 16-bit residual 315-318; 4096 x
-// 3584 x 2 x 6144 SwiGLU 251-262 (library 245), SiTU-GLU 273-286.  Matrix
-// cores busy for 76% of the kernel; 8192^3 reaches 1491 TFLOP/s, where clocks
-// give way to power.  The rest is the last
-// turn of tiles (448 on 256 CUs) and the epilogue, which nothing overlaps as
-// a CU holds one block.
-template <bool F16, bool GATED>
-__global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(1, 1))) void k_linear_big(LinearParams p, int tn,
-                                                                                               int tt, int ksplit)
+// ------------------------------------------------------------------- groups
+
+// Products of groups: a block finds its tile of TM rows by the groups' offsets
+// (each wave for itself: a lane counts the tiles of 1/64 of the groups, a scan
+// over the lanes adds them up), and p becomes the group's: its weights, and M
+// the end of its rows.  Offsets outside [0, M] are taken as its ends.  The
+// launch has blocks for the most tiles that any offsets make; false: this one
+// has none.
+template <int TM, class P>
+__device__ __forceinline__ bool block_tile(P &p, int tn, int tt, int &t0, int &ni)
 {
-    using V = typename Frag<F16>::V;
-    __shared__ __align__(1024) uint8_t lds_blk[kBigLds];
-    LDS uint8_t *lds = (LDS uint8_t *)lds_blk;
-    const int lane = threadIdx.x & 63, wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    int ti, ni;
-    tile_of(blockIdx.x % (tn * tt), tn, tt, ni, ti);
-    const int t0 = ti * 256, n0 = ni * (GATED ? 128 : 256);
-    // the block's part of K
-    const int ks = blockIdx.x / (tn * tt), SA = (p.K + 63) / 64;
-    const int kb = (int)((int64_t)SA * ks / ksplit) * 64, K = min(p.K, (int)((int64_t)SA * (ks + 1) / ksplit) * 64) - kb;
-    const uint16_t *W = reinterpret_cast<const uint16_t *>(p.w) + kb, *U = reinterpret_cast<const uint16_t *>(p.w_up) + kb;
-    const uint16_t *X = reinterpret_cast<const uint16_t *>(p.x) + kb + (size_t)t0 * p.ldx;
-    const int na1 = n0 + 128;
-    const __amdgpu_buffer_rsrc_t rA0 = rows_rsrc(W + (size_t)n0 * p.ldw, min(128, p.N - n0), p.ldw, K);
-    const __amdgpu_buffer_rsrc_t rA1 =
-        GATED ? rows_rsrc(U + (size_t)n0 * p.ldw, min(128, p.N - n0), p.ldw, K)
-              : rows_rsrc(na1 < p.N ? W + (size_t)na1 * p.ldw : W, min(128, p.N - na1), p.ldw, K);
-    const __amdgpu_buffer_rsrc_t rB0 = rows_rsrc(X, min(128, p.M - t0), p.ldx, K);
-    const __amdgpu_buffer_rsrc_t rB1 =
-        rows_rsrc(t0 + 128 < p.M ? X + (size_t)128 * p.ldx : X, min(128, p.M - t0 - 128), p.ldx, K);
-
-    // copies: the wave's 32 rows of a unit in four pieces of 8, this lane's 16 bytes of each
-    const int l8 = lane >> 3, piece = (lane & 7) ^ (l8 >> 1);
-    uint32_t va[4], vb[4];
-#pragma unroll
-    for (int j = 0; j < 4; j++) {
-        const uint32_t row = 32 * wv + 8 * j + l8, col = (piece ^ (j & 1 ? 4 : 0)) * 16;
-        va[j] = (uint32_t)(row * p.ldw * 2) + col;
-        vb[j] = (uint32_t)(row * p.ldx * 2) + col;
-    }
-    int kc0 = piece * 8, kc1 = (piece ^ 4) * 8;
-    const uint32_t m0w = (uint32_t)(uintptr_t)lds + wv * 4096;
-    // unit positions in a stage's buffer
-    constexpr int A0 = 0, A1 = kUnit, B0 = 2 * kUnit, B1 = 3 * kUnit, BUF = 4 * kUnit;
-    // piece j of the wave's part of a unit, D stages on (checked where that stage may end past K)
-    auto copy = [&](auto check, auto d, __amdgpu_buffer_rsrc_t r, int at, bool b, int j) {
-        constexpr int D = decltype(d)::value;
-        uint32_t v = (b ? vb[j] : va[j]) + D * 128;
-        if (decltype(check)::value) v = (j & 1 ? kc1 : kc0) + D * 64 < K ? v : 0x80000000u;
-        copy16(r, m0w + at + j * 1024, v);
-    };
-
-    // fragment reads: lane l holds row l % 16 of a 16-row tile, the k pieces l / 16 and 4 + l / 16 of a stage
-    const int r16 = lane & 15, q4 = lane >> 4;
-    const int wn = wv >> 1, wt = wv & 1;
-    const LDS uint8_t *fa[2], *fb[2];  // in the buffer that is read next
-#pragma unroll
-    for (int st = 0; st < 2; st++) {
-        const int o = r16 * 128 + (((st * 4 + q4) ^ (r16 >> 1)) << 4);
-        fa[st] = lds + wn * 64 * 128 + o;
-        fb[st] = lds + wt * 64 * 128 + o;
-    }
-    V a0[2][4], a1[2][4], b0[2][4], b1[2][4];
-    auto readA = [&](V(&a)[2][4], int at, int i) { a[i >> 2][i & 3] = __builtin_bit_cast(V, lds_ld16(fa[i >> 2] + at + (i & 3) * 2048)); };
-    auto readB = [&](V(&b)[2][4], int at, int i) { b[i >> 2][i & 3] = __builtin_bit_cast(V, lds_ld16(fb[i >> 2] + at + (i & 3) * 2048)); };
-    auto turn = [&](const LDS uint8_t *(&q)[2], int d) { q[0] += d; q[1] += d; };
-    f32x4_t acc[2][2][4][4] = {};  // [A half][B half][16 n][16 tokens]
-
-    using Yes = std::true_type;
-    using No = std::false_type;
-    using D0 = std::integral_constant<int, 0>;
-    using D1 = std::integral_constant<int, 1>;
-    using D2 = std::integral_constant<int, 2>;
-    using D3 = std::integral_constant<int, 3>;
-    auto unit = [&](auto d, __amdgpu_buffer_rsrc_t r, int at, bool b) {
-#pragma unroll
-        for (int j = 0; j < 4; j++) copy(Yes{}, d, r, at, b, j);
-    };
-    unit(D0{}, rA0, A0, false);
-    unit(D0{}, rB0, B0, true);
-    unit(D0{}, rB1, B1, true);
-    unit(D0{}, rA1, A1, false);
-    unit(D1{}, rA0, BUF + A0, false);
-    unit(D1{}, rB1, BUF + B1, true);
-    unit(D1{}, rB0, BUF + B0, true);
-    unit(D1{}, rA1, BUF + A1, false);
-    wait_copies<24>();
-    barrier();
-#pragma unroll
-    for (int i = 0; i < 8; i++) {
-        readA(a0, A0, i);
-        readB(b0, B0, i);
-    }
-    wait_copies<24>();  // (these reads too: the first two phases fill the units anew)
-
-    // A phase multiplies one A half with one B half (64 n x 64 tokens x 64 k
-    // per wave: 32 products).  Spread between them go the reads of the half
-    // the next phase needs, and the copies, two stages on, of the unit whose
-    // last reads were issued two phases before: every unit is filled six
-    // phases before it is read.
-    auto phase = [&](auto check, auto d, __amdgpu_buffer_rsrc_t r, int at, bool b, f32x4_t(&c)[4][4], const V(&x)[2][4],
-                     const V(&y)[2][4], auto read) {
-        __builtin_amdgcn_sched_barrier(0);
-        wait_copies<20, 8>();
-        barrier();
-        __builtin_amdgcn_sched_barrier(0);
-#pragma unroll
-        for (int i = 0; i < 32; i++) {
-            const int st = i >> 4, f = (i >> 2) & 3, g = f & 1 ? 3 - (i & 3) : i & 3;
-            mfma16(x[st][f], y[st][g], c[f][g]);
-            if (i % 4 == 0) read(i >> 2);
-            if (i % 8 == 2) copy(check, d, r, at, b, i >> 3);
-            __builtin_amdgcn_sched_barrier(0);
+    if constexpr (!P::grouped) {
+        int ti;
+        tile_of(blockIdx.x % (tn * tt), tn, tt, ni, ti);
+        t0 = ti * TM;
+        return true;
+    } else {
+        const int lane = threadIdx.x & 63, per = (p.groups + 63) >> 6, g0 = lane * per;
+        auto start = [&](int g) { return min(max(p.offsets[min(g, p.groups)], 0), p.M); };
+        int mine = 0;
+        for (int i = 0, a = start(g0); i < per; i++) {
+            const int b = start(g0 + i + 1);
+            mine += (max(b - a, 0) + TM - 1) / TM;
+            a = b;
         }
-    };
-    auto two_stages = [&](auto check) {
-        // stage s: B0 first
-        phase(check, D2{}, rA0, A0, false, acc[0][0], a0, b0, [&](int i) { readB(b1, B1, i); });
-        phase(check, D2{}, rB0, B0, true, acc[0][1], a0, b1, [&](int i) { readA(a1, A1, i); });
-        turn(fa, BUF);
-        phase(check, D2{}, rB1, B1, true, acc[1][1], a1, b1, [&](int i) { readA(a0, A0, i); });
-        turn(fb, BUF);
-        phase(check, D2{}, rA1, A1, false, acc[1][0], a1, b0, [&](int i) { readB(b1, B1, i); });
-        // stage s + 1: B1 first
-        phase(check, D3{}, rA0, BUF + A0, false, acc[0][1], a0, b1, [&](int i) { readB(b0, B0, i); });
-        phase(check, D3{}, rB1, BUF + B1, true, acc[0][0], a0, b0, [&](int i) { readA(a1, A1, i); });
-        turn(fa, -BUF);
-        phase(check, D3{}, rB0, BUF + B0, true, acc[1][0], a1, b0, [&](int i) { readA(a0, A0, i); });
-        turn(fb, -BUF);
-        phase(check, D3{}, rA1, BUF + A1, false, acc[1][1], a1, b1, [&](int i) { readB(b0, B0, i); });
+        int upto = mine;
 #pragma unroll
-        for (int j = 0; j < 4; j++) va[j] += 256, vb[j] += 256;
-        kc0 += 128;
-        kc1 += 128;
-    };
-    // (the copies of stages up to s + 3 stay inside K while 64 (s + 4) <= K)
-    const int S = (K + 63) / 64;
-    int s = 0;
-    for (; 64 * (s + 4) <= K; s += 2) two_stages(No{});
-    for (; s < S; s += 2) two_stages(Yes{});
-    __builtin_amdgcn_sched_barrier(0);
-    // The last products' results: nobody else waits for written-out products,
-    // so every sum goes through a statement behind the wait.
-    asm volatile("s_nop 15\n\ts_nop 15" ::: "memory");
-#pragma unroll
-    for (int i = 0; i < 4; i++) {
-        f32x4_t(&c)[4][4] = acc[i >> 1][i & 1];
-        asm volatile(""
-                     : "+a"(c[0][0]), "+a"(c[0][1]), "+a"(c[0][2]), "+a"(c[0][3]), "+a"(c[1][0]), "+a"(c[1][1]), "+a"(c[1][2]),
-                       "+a"(c[1][3]), "+a"(c[2][0]), "+a"(c[2][1]), "+a"(c[2][2]), "+a"(c[2][3]), "+a"(c[3][0]), "+a"(c[3][1]),
-                       "+a"(c[3][2]), "+a"(c[3][3]));
+        for (int d = 1; d < 64; d <<= 1) {
+            const int v = __shfl_up(upto, d, 64);
+            if (lane >= d) upto += v;
+        }
+        const int tiles = __builtin_amdgcn_readlane(upto, 63);
+        const int per8 = tn * tiles, x = blockIdx.x & 7;
+        if ((int)(blockIdx.x >> 3) >= (per8 >> 3) + (x < (per8 & 7) ? 1 : 0)) return false;
+        int ti;
+        tile_of(blockIdx.x, tn, tiles, ni, ti);
+        const uint64_t past = __ballot(upto > ti);
+        if (!past) return false;
+        const int owner = __builtin_ctzll(past);
+        int left = ti - (upto - mine), g = 0, first = 0, end = 0;
+        for (int i = 0, a = start(g0); i < per; i++) {
+            const int b = start(g0 + i + 1), n = (max(b - a, 0) + TM - 1) / TM;
+            if (left >= 0 && left < n) g = g0 + i, first = a + left * TM, end = b;
+            left -= n;
+            a = b;
+        }
+        g = __builtin_amdgcn_readlane(g, owner);
+        t0 = __builtin_amdgcn_readlane(first, owner);
+        p.M = __builtin_amdgcn_readlane(end, owner);
+        p.w = reinterpret_cast<const uint16_t *>(p.w) + g * p.wstride;
+        if (p.w_up) p.w_up = reinterpret_cast<const uint16_t *>(p.w_up) + g * p.wstride;
+        const int64_t bias = g * p.bstride * (p.bias_f32 ? 4 : 2);
+        if (p.bias) p.bias = reinterpret_cast<const char *>(p.bias) + bias;
+        if (p.bias_up) p.bias_up = reinterpret_cast<const char *>(p.bias_up) + bias;
+        if constexpr (P::mx) {
+            p.ws += g * p.sstride;
+            if (p.us) p.us += g * p.sstride;
+        }
+        return true;
     }
-    wait_copies<0>();
-    barrier();
+}
 
+template <class P>
+__device__ __forceinline__ bool gathered(const P &p)
+{
+    if constexpr (P::grouped) return p.rows != nullptr;
+    return false;
+}
+template <class P>
+__device__ __forceinline__ int x_rows(const P &p)
+{
+    if constexpr (P::grouped) return p.xrows;
+    return p.M;
+}
+// the row of x behind row t (-1: none)
+template <class P>
+__device__ __forceinline__ int x_source(const P &p, int t)
+{
+    if constexpr (P::grouped) {
+        if (t >= p.M) return -1;
+        const int r = p.rows[t];
+        return (uint32_t)r < (uint32_t)p.xrows ? r : -1;
+    }
+    return t;
+}
+// where row `row` of the tile at t0 starts, in bytes from the tile's first row
+// or, gathered, from x's (all of x below 2 GiB then): past every buffer where
+// it has no source
+template <class P>
+__device__ __forceinline__ uint32_t x_row(const P &p, int t0, int row)
+{
+    if (!gathered(p)) return (uint32_t)(row * p.ldx * 2);
+    const int r = x_source(p, t0 + row);
+    return r < 0 ? 0x80000000u : (uint32_t)(r * p.ldx * 2);
+}
+
+// The end of a 256 x 256 tile: a wave's sums acc[A half][B half][16 n][16
+// tokens] to the outputs (ks of ksplit: to the partial sums).
+template <bool F16, bool GATED, class P>
+__device__ __forceinline__ void finish_big(const P &p, LDS uint8_t *lds, const f32x4_t (&acc)[2][2][4][4], int t0, int n0, int ks,
+                                           int ksplit)
+{
+    const int lane = threadIdx.x & 63, wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int r16 = lane & 15, q4 = lane >> 4, wn = wv >> 1, wt = wv & 1;
     // epilogue: 64 n x 128 tokens of sums (gated: 64 tokens of both matrices)
     // at a time through the wave's own LDS, so that a row's 64 outputs leave
     // as 16 lanes x 4
@@ -614,7 +564,374 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(1, 1))) voi
                 __builtin_amdgcn_sched_barrier(0);
             }
         }
+    }}
+
+// 256 x 256 outputs (gated: 128 of each matrix) per block and CU, four waves
+// of 128 x 128, one to a SIMD, whose 256 sums per lane fill the accumulation
+// registers: 64 products of 16 x 16 x 32 per 32 fragment reads of 16 bytes,
+// so LDS supplies half of what it could, and the matrix cores are the bound.
+// 16 x 16 x 32 and not 32 x 32 x 16: on registers alone the whole chip does
+// 2050 TFLOP/s with the former and 1660-1850 with the latter, which draws
+// more power (4096 x 7168 x 7168: 372 us with the latter, 325 with the former).
+// Measured: 4096 x 7168 x 7168 296-309 us by the box (1422-1360 TFLOP/s, the
+// library's product 285-293), with bias and a 16-bit residual 315-318; 4096 x
+// 3584 x 2 x 6144 SwiGLU 251-262 (library 245), SiTU-GLU 273-286.  Matrix
+// cores busy for 76% of the kernel; 8192^3 reaches 1491 TFLOP/s, where clocks
+// give way to power.  The rest is the last
+// turn of tiles (448 on 256 CUs) and the epilogue, which nothing overlaps as
+// a CU holds one block.
+template <bool F16, bool GATED, class P>
+__global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(1, 1))) void k_linear_big(P p, int tn, int tt, int ksplit)
+{
+    using V = typename Frag<F16>::V;
+    __shared__ __align__(1024) uint8_t lds_blk[kBigLds];
+    LDS uint8_t *lds = (LDS uint8_t *)lds_blk;
+    const int lane = threadIdx.x & 63, wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    int t0, ni;
+    if (!block_tile<256>(p, tn, tt, t0, ni)) return;
+    const int n0 = ni * (GATED ? 128 : 256);
+    // the block's part of K
+    const int ks = P::grouped ? 0 : blockIdx.x / (tn * tt), SA = (p.K + 63) / 64;
+    const int kb = (int)((int64_t)SA * ks / ksplit) * 64, K = min(p.K, (int)((int64_t)SA * (ks + 1) / ksplit) * 64) - kb;
+    const uint16_t *W = reinterpret_cast<const uint16_t *>(p.w) + kb, *U = reinterpret_cast<const uint16_t *>(p.w_up) + kb;
+    const bool gather = gathered(p);
+    const uint16_t *X = reinterpret_cast<const uint16_t *>(p.x) + kb + (gather ? 0 : (size_t)t0 * p.ldx);
+    const int na1 = n0 + 128;
+    const __amdgpu_buffer_rsrc_t rA0 = rows_rsrc(W + (size_t)n0 * p.ldw, min(128, p.N - n0), p.ldw, K);
+    const __amdgpu_buffer_rsrc_t rA1 =
+        GATED ? rows_rsrc(U + (size_t)n0 * p.ldw, min(128, p.N - n0), p.ldw, K)
+              : rows_rsrc(na1 < p.N ? W + (size_t)na1 * p.ldw : W, min(128, p.N - na1), p.ldw, K);
+    const __amdgpu_buffer_rsrc_t rB0 = rows_rsrc(X, gather ? x_rows(p) : min(128, p.M - t0), p.ldx, K);
+    const __amdgpu_buffer_rsrc_t rB1 =
+        gather ? rB0 : rows_rsrc(t0 + 128 < p.M ? X + (size_t)128 * p.ldx : X, min(128, p.M - t0 - 128), p.ldx, K);
+
+    // copies: the wave's 32 rows of a unit in four pieces of 8, this lane's 16 bytes of each
+    const int l8 = lane >> 3, piece = (lane & 7) ^ (l8 >> 1);
+    uint32_t va[4], vb[4], vg[4];  // vg: of the second half of gathered rows
+#pragma unroll
+    for (int j = 0; j < 4; j++) {
+        const uint32_t row = 32 * wv + 8 * j + l8, col = (piece ^ (j & 1 ? 4 : 0)) * 16;
+        va[j] = (uint32_t)(row * p.ldw * 2) + col;
+        vb[j] = x_row(p, t0, row) + col;
+        if (P::grouped) vg[j] = (gather ? x_row(p, t0, row + 128) : (uint32_t)(row * p.ldx * 2)) + col;
     }
+    int kc0 = piece * 8, kc1 = (piece ^ 4) * 8;
+    const uint32_t m0w = (uint32_t)(uintptr_t)lds + wv * 4096;
+    // unit positions in a stage's buffer
+    constexpr int A0 = 0, A1 = kUnit, B0 = 2 * kUnit, B1 = 3 * kUnit, BUF = 4 * kUnit;
+    // piece j of the wave's part of a unit, D stages on (checked where that stage may end past K)
+    auto copy = [&](auto check, auto d, __amdgpu_buffer_rsrc_t r, int at, bool b, int j) {
+        constexpr int D = decltype(d)::value;
+        uint32_t v = (b ? (P::grouped && (at == B1 || at == BUF + B1) ? vg[j] : vb[j]) : va[j]) + D * 128;
+        if (decltype(check)::value) v = (j & 1 ? kc1 : kc0) + D * 64 < K ? v : 0x80000000u;
+        copy16(r, m0w + at + j * 1024, v);
+    };
+
+    // fragment reads: lane l holds row l % 16 of a 16-row tile, the k pieces l / 16 and 4 + l / 16 of a stage
+    const int r16 = lane & 15, q4 = lane >> 4;
+    const int wn = wv >> 1, wt = wv & 1;
+    const LDS uint8_t *fa[2], *fb[2];  // in the buffer that is read next
+#pragma unroll
+    for (int st = 0; st < 2; st++) {
+        const int o = r16 * 128 + (((st * 4 + q4) ^ (r16 >> 1)) << 4);
+        fa[st] = lds + wn * 64 * 128 + o;
+        fb[st] = lds + wt * 64 * 128 + o;
+    }
+    V a0[2][4], a1[2][4], b0[2][4], b1[2][4];
+    auto readA = [&](V(&a)[2][4], int at, int i) { a[i >> 2][i & 3] = __builtin_bit_cast(V, lds_ld16(fa[i >> 2] + at + (i & 3) * 2048)); };
+    auto readB = [&](V(&b)[2][4], int at, int i) { b[i >> 2][i & 3] = __builtin_bit_cast(V, lds_ld16(fb[i >> 2] + at + (i & 3) * 2048)); };
+    auto turn = [&](const LDS uint8_t *(&q)[2], int d) { q[0] += d; q[1] += d; };
+    f32x4_t acc[2][2][4][4] = {};  // [A half][B half][16 n][16 tokens]
+
+    using Yes = std::true_type;
+    using No = std::false_type;
+    using D0 = std::integral_constant<int, 0>;
+    using D1 = std::integral_constant<int, 1>;
+    using D2 = std::integral_constant<int, 2>;
+    using D3 = std::integral_constant<int, 3>;
+    auto unit = [&](auto d, __amdgpu_buffer_rsrc_t r, int at, bool b) {
+#pragma unroll
+        for (int j = 0; j < 4; j++) copy(Yes{}, d, r, at, b, j);
+    };
+    unit(D0{}, rA0, A0, false);
+    unit(D0{}, rB0, B0, true);
+    unit(D0{}, rB1, B1, true);
+    unit(D0{}, rA1, A1, false);
+    unit(D1{}, rA0, BUF + A0, false);
+    unit(D1{}, rB1, BUF + B1, true);
+    unit(D1{}, rB0, BUF + B0, true);
+    unit(D1{}, rA1, BUF + A1, false);
+    wait_copies<24>();
+    barrier();
+#pragma unroll
+    for (int i = 0; i < 8; i++) {
+        readA(a0, A0, i);
+        readB(b0, B0, i);
+    }
+    wait_copies<24>();  // (these reads too: the first two phases fill the units anew)
+
+    // A phase multiplies one A half with one B half (64 n x 64 tokens x 64 k
+    // per wave: 32 products).  Spread between them go the reads of the half
+    // the next phase needs, and the copies, two stages on, of the unit whose
+    // last reads were issued two phases before: every unit is filled six
+    // phases before it is read.
+    auto phase = [&](auto check, auto d, __amdgpu_buffer_rsrc_t r, int at, bool b, f32x4_t(&c)[4][4], const V(&x)[2][4],
+                     const V(&y)[2][4], auto read) {
+        __builtin_amdgcn_sched_barrier(0);
+        wait_copies<20, 8>();
+        barrier();
+        __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+        for (int i = 0; i < 32; i++) {
+            const int st = i >> 4, f = (i >> 2) & 3, g = f & 1 ? 3 - (i & 3) : i & 3;
+            mfma16(x[st][f], y[st][g], c[f][g]);
+            if (i % 4 == 0) read(i >> 2);
+            if (i % 8 == 2) copy(check, d, r, at, b, i >> 3);
+            __builtin_amdgcn_sched_barrier(0);
+        }
+    };
+    auto two_stages = [&](auto check) {
+        // stage s: B0 first
+        phase(check, D2{}, rA0, A0, false, acc[0][0], a0, b0, [&](int i) { readB(b1, B1, i); });
+        phase(check, D2{}, rB0, B0, true, acc[0][1], a0, b1, [&](int i) { readA(a1, A1, i); });
+        turn(fa, BUF);
+        phase(check, D2{}, rB1, B1, true, acc[1][1], a1, b1, [&](int i) { readA(a0, A0, i); });
+        turn(fb, BUF);
+        phase(check, D2{}, rA1, A1, false, acc[1][0], a1, b0, [&](int i) { readB(b1, B1, i); });
+        // stage s + 1: B1 first
+        phase(check, D3{}, rA0, BUF + A0, false, acc[0][1], a0, b1, [&](int i) { readB(b0, B0, i); });
+        phase(check, D3{}, rB1, BUF + B1, true, acc[0][0], a0, b0, [&](int i) { readA(a1, A1, i); });
+        turn(fa, -BUF);
+        phase(check, D3{}, rB0, BUF + B0, true, acc[1][0], a1, b0, [&](int i) { readA(a0, A0, i); });
+        turn(fb, -BUF);
+        phase(check, D3{}, rA1, BUF + A1, false, acc[1][1], a1, b1, [&](int i) { readB(b0, B0, i); });
+#pragma unroll
+        for (int j = 0; j < 4; j++) {
+            va[j] += 256, vb[j] += 256;
+            if (P::grouped) vg[j] += 256;
+        }
+        kc0 += 128;
+        kc1 += 128;
+    };
+    // (the copies of stages up to s + 3 stay inside K while 64 (s + 4) <= K)
+    const int S = (K + 63) / 64;
+    int s = 0;
+    for (; 64 * (s + 4) <= K; s += 2) two_stages(No{});
+    for (; s < S; s += 2) two_stages(Yes{});
+    __builtin_amdgcn_sched_barrier(0);
+    // The last products' results: nobody else waits for written-out products,
+    // so every sum goes through a statement behind the wait.
+    asm volatile("s_nop 15\n\ts_nop 15" ::: "memory");
+#pragma unroll
+    for (int i = 0; i < 4; i++) {
+        f32x4_t(&c)[4][4] = acc[i >> 1][i & 1];
+        asm volatile(""
+                     : "+a"(c[0][0]), "+a"(c[0][1]), "+a"(c[0][2]), "+a"(c[0][3]), "+a"(c[1][0]), "+a"(c[1][1]), "+a"(c[1][2]),
+                       "+a"(c[1][3]), "+a"(c[2][0]), "+a"(c[2][1]), "+a"(c[2][2]), "+a"(c[2][3]), "+a"(c[3][0]), "+a"(c[3][1]),
+                       "+a"(c[3][2]), "+a"(c[3][3]));
+    }
+    wait_copies<0>();
+    barrier();
+
+    finish_big<F16, GATED>(p, lds, acc, t0, n0, ks, ksplit);
+}
+
+// ------------------------------------------- whole prompts: 256 x 256, MXFP4
+
+// c += a b, 16 x 16 x 128 codes and a scale for each lane's 32, c in accumulation registers
+__device__ __forceinline__ void mfma16_mx(u32x4_t a, int sa, u32x4_t b, int sb, f32x4_t &c)
+{
+    asm volatile("v_mfma_scale_f32_16x16x128_f8f6f4 %0, %1, %2, %0, %3, %4 op_sel_hi:[0,0,0] cbsz:4 blgp:4"
+                 : "+a"(c)
+                 : "v"(a), "v"(b), "v"(sa), "v"(sb));
+}
+
+constexpr int kMxUnit = kUnit + 128 * 8;  // 128 rows x 256 codes and their scales
+constexpr int kMxLds = 4 * kBigWave > 8 * kMxUnit ? 4 * kBigWave : 8 * kMxUnit;
+
+// k_linear_big's tile and turn of phases on MXFP4 operands: a stage's 128
+// bytes of a row are 256 codes, and one product takes 128 of them in the
+// cycles of a 16-bit one's 32.  The 8 scales of a row and stage are copied
+// behind their unit; a lane's products take one byte each, read from there.
+template <bool F16, bool GATED, class P>
+__global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(1, 1))) void k_mx_big(P p, int tn, int tt, int ksplit)
+{
+    __shared__ __align__(1024) uint8_t lds_blk[kMxLds];
+    LDS uint8_t *lds = (LDS uint8_t *)lds_blk;
+    const int lane = threadIdx.x & 63, wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    int t0, ni;
+    if (!block_tile<256>(p, tn, tt, t0, ni)) return;
+    const int n0 = ni * (GATED ? 128 : 256);
+    const int ks = P::grouped ? 0 : blockIdx.x / (tn * tt), SA = (p.K + 63) / 64;
+    const int kb = (int)((int64_t)SA * ks / ksplit) * 64, K = min(p.K, (int)((int64_t)SA * (ks + 1) / ksplit) * 64) - kb;
+    const uint16_t *W = reinterpret_cast<const uint16_t *>(p.w) + kb, *U = reinterpret_cast<const uint16_t *>(p.w_up) + kb;
+    const bool gather = gathered(p);
+    const uint16_t *X = reinterpret_cast<const uint16_t *>(p.x) + kb + (gather ? 0 : (size_t)t0 * p.ldx);
+    const uint8_t *WS = p.ws + (kb >> 3), *US = GATED ? p.us + (kb >> 3) : nullptr;
+    const uint8_t *XS = p.xs + (kb >> 3) + (gather ? 0 : (size_t)t0 * p.ldxs);
+    const int na1 = GATED ? n0 : n0 + 128, ra0 = min(128, p.N - n0), ra1 = min(128, p.N - na1), at1 = ra1 > 0 ? na1 : 0;
+    const int xr = x_rows(p), rb0 = gather ? xr : min(128, p.M - t0), rb1 = gather ? xr : min(128, p.M - t0 - 128);
+    const int bt1 = gather || rb1 <= 0 ? 0 : 128;
+    auto scales_rsrc = [&](const uint8_t *base, int rows, int64_t ld) {
+        return grsrc(base, rows > 0 ? (uint32_t)((rows - 1) * ld + (((K >> 3) + 3) & ~3)) : 0u);
+    };
+    const __amdgpu_buffer_rsrc_t rA0 = rows_rsrc(W + (size_t)n0 * p.ldw, ra0, p.ldw, K);
+    const __amdgpu_buffer_rsrc_t rA1 = rows_rsrc((GATED ? U : W) + (size_t)at1 * p.ldw, ra1, p.ldw, K);
+    const __amdgpu_buffer_rsrc_t rB0 = rows_rsrc(X, rb0, p.ldx, K);
+    const __amdgpu_buffer_rsrc_t rB1 = rows_rsrc(X + (size_t)bt1 * p.ldx, rb1, p.ldx, K);
+    const __amdgpu_buffer_rsrc_t sA0 = scales_rsrc(WS + (size_t)n0 * p.ldws, ra0, p.ldws);
+    const __amdgpu_buffer_rsrc_t sA1 = scales_rsrc((GATED ? US : WS) + (size_t)at1 * p.ldws, ra1, p.ldws);
+    const __amdgpu_buffer_rsrc_t sB0 = scales_rsrc(XS, rb0, p.ldxs);
+    const __amdgpu_buffer_rsrc_t sB1 = scales_rsrc(XS + (size_t)bt1 * p.ldxs, rb1, p.ldxs);
+
+    // copies: the wave's 32 rows of a unit in four pieces of 8, this lane's 16
+    // bytes of each, and half a row's scales
+    const int l8 = lane >> 3, piece = (lane & 7) ^ (l8 >> 1);
+    uint32_t va[4], vb[4], vg[4];
+#pragma unroll
+    for (int j = 0; j < 4; j++) {
+        const uint32_t row = 32 * wv + 8 * j + l8, col = (piece ^ (j & 1 ? 4 : 0)) * 16;
+        va[j] = (uint32_t)(row * p.ldw * 2) + col;
+        vb[j] = x_row(p, t0, row) + col;
+        if (P::grouped) vg[j] = (gather ? x_row(p, t0, row + 128) : (uint32_t)(row * p.ldx * 2)) + col;
+    }
+    const int srow = 32 * wv + (lane >> 1), sh = (lane & 1) * 4;
+    auto scale_row = [&](int row) {
+        const int r = gather ? x_source(p, t0 + row) : srow;
+        return (r < 0 ? 0x80000000u : (uint32_t)(r * p.ldxs)) + sh;
+    };
+    uint32_t vas = (uint32_t)(srow * p.ldws) + sh, vbs = scale_row(srow), vgs = P::grouped ? scale_row(srow + 128) : vbs;
+    int kc0 = piece * 8, kc1 = (piece ^ 4) * 8, kcs = sh * 8;
+    const uint32_t m0w = (uint32_t)(uintptr_t)lds + wv * 4096, m0s = (uint32_t)(uintptr_t)lds + kUnit + wv * 256;
+    constexpr int A0 = 0, A1 = kMxUnit, B0 = 2 * kMxUnit, B1 = 3 * kMxUnit, BUF = 4 * kMxUnit;
+    // piece j of the wave's part of a unit, its scales as piece 4, D stages on
+    // (checked where that stage may end past K)
+    auto copy = [&](auto check, auto d, __amdgpu_buffer_rsrc_t r, __amdgpu_buffer_rsrc_t s, int at, bool b, int j) {
+        constexpr int D = decltype(d)::value;
+        const bool second = P::grouped && (at == B1 || at == BUF + B1);
+        if (j < 4) {
+            uint32_t v = (b ? (second ? vg[j] : vb[j]) : va[j]) + D * 128;
+            if (decltype(check)::value) v = (j & 1 ? kc1 : kc0) + D * 64 < K ? v : 0x80000000u;
+            copy16(r, m0w + at + j * 1024, v);
+        } else {
+            uint32_t v = (b ? (second ? vgs : vbs) : vas) + D * 8;
+            if (decltype(check)::value) v = kcs + D * 64 < K ? v : 0x80000000u;
+            copy4(s, m0s + at, v);
+        }
+    };
+
+    const int r16 = lane & 15, q4 = lane >> 4;
+    const int wn = wv >> 1, wt = wv & 1;
+    const LDS uint8_t *fa[3], *fb[3];  // in the buffer that is read next: fragments of both steps, scales
+#pragma unroll
+    for (int st = 0; st < 2; st++) {
+        const int o = r16 * 128 + (((st * 4 + q4) ^ (r16 >> 1)) << 4);
+        fa[st] = lds + wn * 64 * 128 + o;
+        fb[st] = lds + wt * 64 * 128 + o;
+    }
+    fa[2] = lds + kUnit + (wn * 64 + r16) * 8 + q4;
+    fb[2] = lds + kUnit + (wt * 64 + r16) * 8 + q4;
+    struct Half {  // 64 rows x 256 codes: [step][16 rows]
+        u32x4_t f[2][4];
+        int s[2][4];
+    };
+    Half a0, a1, b0, b1;
+    auto fetch = [&](Half &h, const LDS uint8_t *const(&q)[3], int at, int i) {
+        h.s[i >> 2][i & 3] = q[2][at + (i & 3) * 128 + (i >> 2) * 4];
+        h.f[i >> 2][i & 3] = __builtin_bit_cast(u32x4_t, lds_ld16(q[i >> 2] + at + (i & 3) * 2048));
+    };
+    auto readA = [&](Half &a, int at, int i) { fetch(a, fa, at, i); };
+    auto readB = [&](Half &b, int at, int i) { fetch(b, fb, at, i); };
+    auto turn = [&](const LDS uint8_t *(&q)[3], int d) { q[0] += d; q[1] += d; q[2] += d; };
+    f32x4_t acc[2][2][4][4] = {};  // [A half][B half][16 n][16 tokens]
+
+    using Yes = std::true_type;
+    using No = std::false_type;
+    using D0 = std::integral_constant<int, 0>;
+    using D1 = std::integral_constant<int, 1>;
+    using D2 = std::integral_constant<int, 2>;
+    using D3 = std::integral_constant<int, 3>;
+    auto unit = [&](auto d, __amdgpu_buffer_rsrc_t r, __amdgpu_buffer_rsrc_t s, int at, bool b) {
+#pragma unroll
+        for (int j = 0; j < 5; j++) copy(Yes{}, d, r, s, at, b, j);
+    };
+    unit(D0{}, rA0, sA0, A0, false);
+    unit(D0{}, rB0, sB0, B0, true);
+    unit(D0{}, rB1, sB1, B1, true);
+    unit(D0{}, rA1, sA1, A1, false);
+    unit(D1{}, rA0, sA0, BUF + A0, false);
+    unit(D1{}, rB1, sB1, BUF + B1, true);
+    unit(D1{}, rB0, sB0, BUF + B0, true);
+    unit(D1{}, rA1, sA1, BUF + A1, false);
+    wait_copies<30>();
+    barrier();
+#pragma unroll
+    for (int i = 0; i < 8; i++) {
+        readA(a0, A0, i);
+        readB(b0, B0, i);
+    }
+    wait_copies<30>();  // (these reads too: the first two phases fill the units anew)
+
+    // the phases of k_linear_big; a read is one of a fragment and one of its scales
+    auto phase = [&](auto check, auto d, __amdgpu_buffer_rsrc_t r, __amdgpu_buffer_rsrc_t s, int at, bool b, f32x4_t(&c)[4][4],
+                     const Half &x, const Half &y, auto read) {
+        __builtin_amdgcn_sched_barrier(0);
+        wait_copies<25, 14>();
+        barrier();
+        __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+        for (int i = 0; i < 32; i++) {
+            const int st = i >> 4, f = (i >> 2) & 3, g = f & 1 ? 3 - (i & 3) : i & 3;
+            mfma16_mx(x.f[st][f], x.s[st][f], y.f[st][g], y.s[st][g], c[f][g]);
+            if (i % 4 == 0) read(i >> 2);
+            if (i % 6 == 2 && i < 30) copy(check, d, r, s, at, b, i / 6);
+            __builtin_amdgcn_sched_barrier(0);
+        }
+    };
+    auto two_stages = [&](auto check) {
+        // stage s: B0 first
+        phase(check, D2{}, rA0, sA0, A0, false, acc[0][0], a0, b0, [&](int i) { readB(b1, B1, i); });
+        phase(check, D2{}, rB0, sB0, B0, true, acc[0][1], a0, b1, [&](int i) { readA(a1, A1, i); });
+        turn(fa, BUF);
+        phase(check, D2{}, rB1, sB1, B1, true, acc[1][1], a1, b1, [&](int i) { readA(a0, A0, i); });
+        turn(fb, BUF);
+        phase(check, D2{}, rA1, sA1, A1, false, acc[1][0], a1, b0, [&](int i) { readB(b1, B1, i); });
+        // stage s + 1: B1 first
+        phase(check, D3{}, rA0, sA0, BUF + A0, false, acc[0][1], a0, b1, [&](int i) { readB(b0, B0, i); });
+        phase(check, D3{}, rB1, sB1, BUF + B1, true, acc[0][0], a0, b0, [&](int i) { readA(a1, A1, i); });
+        turn(fa, -BUF);
+        phase(check, D3{}, rB0, sB0, BUF + B0, true, acc[1][0], a1, b0, [&](int i) { readA(a0, A0, i); });
+        turn(fb, -BUF);
+        phase(check, D3{}, rA1, sA1, BUF + A1, false, acc[1][1], a1, b1, [&](int i) { readB(b0, B0, i); });
+#pragma unroll
+        for (int j = 0; j < 4; j++) {
+            va[j] += 256, vb[j] += 256;
+            if (P::grouped) vg[j] += 256;
+        }
+        vas += 16, vbs += 16, vgs += 16;
+        kc0 += 128;
+        kc1 += 128;
+        kcs += 128;
+    };
+    // (the copies of stages up to s + 3 stay inside K while 64 (s + 4) <= K)
+    const int S = (K + 63) / 64;
+    int s = 0;
+    for (; 64 * (s + 4) <= K; s += 2) two_stages(No{});
+    for (; s < S; s += 2) two_stages(Yes{});
+    __builtin_amdgcn_sched_barrier(0);
+    // (as in k_linear_big: every sum goes through a statement behind the wait)
+    asm volatile("s_nop 15\n\ts_nop 15" ::: "memory");
+#pragma unroll
+    for (int i = 0; i < 4; i++) {
+        f32x4_t(&c)[4][4] = acc[i >> 1][i & 1];
+        asm volatile(""
+                     : "+a"(c[0][0]), "+a"(c[0][1]), "+a"(c[0][2]), "+a"(c[0][3]), "+a"(c[1][0]), "+a"(c[1][1]), "+a"(c[1][2]),
+                       "+a"(c[1][3]), "+a"(c[2][0]), "+a"(c[2][1]), "+a"(c[2][2]), "+a"(c[2][3]), "+a"(c[3][0]), "+a"(c[3][1]),
+                       "+a"(c[3][2]), "+a"(c[3][3]));
+    }
+    wait_copies<0>();
+    barrier();
+    finish_big<F16, GATED>(p, lds, acc, t0, n0, ks, ksplit);
 }
 
 // ------------------------------------------------------- a few hundred tokens
@@ -626,6 +943,17 @@ __device__ __forceinline__ f32x4_t mfma16v(bf16x8_t a, bf16x8_t b, f32x4_t c)
 __device__ __forceinline__ f32x4_t mfma16v(f16x8_t a, f16x8_t b, f32x4_t c)
 {
     return __builtin_amdgcn_mfma_f32_16x16x32_f16(a, b, c, 0, 0, 0);
+}
+
+// 128 codes a row, one scale for a lane's 32
+template <class V>
+__device__ __forceinline__ f32x4_t mfma_mx(V a, int sa, V b, int sb, f32x4_t c)
+{
+    typedef int i32x8_t __attribute__((ext_vector_type(8)));
+    const uint4 x = __builtin_bit_cast(uint4, a), y = __builtin_bit_cast(uint4, b);
+    const i32x8_t xa = {(int)x.x, (int)x.y, (int)x.z, (int)x.w, 0, 0, 0, 0};
+    const i32x8_t yb = {(int)y.x, (int)y.y, (int)y.z, (int)y.w, 0, 0, 0, 0};
+    return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(xa, yb, c, 4, 4, 0, sa, 0, sb);
 }
 
 // TN weight rows (gated: TN / 2 of each matrix) x TM tokens per block, K in a
@@ -643,11 +971,14 @@ __device__ __forceinline__ f32x4_t mfma16v(f16x8_t a, f16x8_t b, f32x4_t c)
 // that are not 16-byte aligned (ANY) go through registers, for both operands:
 // 333 x 1117 x 2049 12.8 and 13.9 us (21, 21), 2048 x 1117 x 2049 38 and 41
 // (27, 27), 2048 x 3585 x 3587 86 and 116 (74, 89).
-template <int TN, int TM, int WN, int WT, int NST>
+// MXFP4 rows: 128 bytes are 256 codes, a stage of the same bytes, and each wave
+// copies 32 rows' scales of it, 8 bytes a row, behind them.
+template <int TN, int TM, int WN, int WT, int NST, bool MX>
 struct Tile {
     static constexpr int NW = WN * WT, THREADS = NW * 64;
-    static constexpr int STAGE = (TN + TM) * 128;
-    static constexpr int CW = STAGE / 1024 / NW;     // copies per wave and stage
+    static constexpr int CODES = (TN + TM) * 128, STAGE = CODES + (MX ? NW * 256 : 0);
+    static constexpr int CW = CODES / 1024 / NW;     // copies per wave and stage
+    static constexpr int CALL = CW + (MX ? 1 : 0);   // with the scales'
     static constexpr int FN = TN / 2 / WN / 16;      // 16-row tiles per wave and half
     static constexpr int FT = TM / WT / 16;
     static constexpr int EN = TN / 2 / WN;           // epilogue: outputs per row of a wave's half
@@ -655,20 +986,22 @@ struct Tile {
     static constexpr int EWAVE = 2 * (TM / WT) * EROW;
     static constexpr int LDSB = NST * STAGE > NW * EWAVE ? NST * STAGE : NW * EWAVE;
     static_assert(TN / 16 % NW == 0 && TM / 8 % NW == 0 && FN >= 1 && FT >= 1 && EN % 16 == 0 && NST >= 3, "tile");
+    static_assert(!MX || ((TN + TM) / 32 <= NW && TN / 2 % 32 == 0), "scales");
 };
 
-template <bool F16, bool GATED, bool ANY, int TN, int TM, int WN, int WT, int NST>
-__global__ __launch_bounds__(WN * WT * 64) void k_linear_tile(LinearParams p, int tn, int tt, int ksplit)
+template <bool F16, bool GATED, bool ANY, int TN, int TM, int WN, int WT, int NST, class P>
+__global__ __launch_bounds__(WN * WT * 64) void k_linear_tile(P p, int tn, int tt, int ksplit)
 {
-    using G = Tile<TN, TM, WN, WT, NST>;
+    using G = Tile<TN, TM, WN, WT, NST, P::mx>;
     using V = typename Frag<F16>::V;
+    static_assert(!(ANY && P::mx), "rows of codes are aligned");
     __shared__ __align__(1024) uint8_t lds_blk[G::LDSB];
     LDS uint8_t *lds = (LDS uint8_t *)lds_blk;
     const int lane = threadIdx.x & 63, wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    int ti, ni;
-    tile_of(blockIdx.x % (tn * tt), tn, tt, ni, ti);
-    const int ks = blockIdx.x / (tn * tt);
-    const int t0 = ti * TM, n0 = ni * (GATED ? TN / 2 : TN);
+    int t0, ni;
+    if (!block_tile<TM>(p, tn, tt, t0, ni)) return;
+    const int ks = P::grouped ? 0 : blockIdx.x / (tn * tt);
+    const int n0 = ni * (GATED ? TN / 2 : TN);
     const int SA = (p.K + 63) / 64, s0 = (int)((int64_t)SA * ks / ksplit), s1 = (int)((int64_t)SA * (ks + 1) / ksplit);
 
     // rows of the two weight halves and of the tokens
@@ -677,8 +1010,9 @@ __global__ __launch_bounds__(WN * WT * 64) void k_linear_tile(LinearParams p, in
     const __amdgpu_buffer_rsrc_t r0 = rows_rsrc(W + (size_t)n0 * p.ldw, min(TN / 2, p.N - n0), p.ldw, p.K);
     const __amdgpu_buffer_rsrc_t r1 =
         rows_rsrc(n1 < p.N ? (GATED ? U : W) + (size_t)n1 * p.ldw : W, min(TN / 2, p.N - n1), p.ldw, p.K);
-    const __amdgpu_buffer_rsrc_t rx =
-        rows_rsrc(reinterpret_cast<const uint16_t *>(p.x) + (size_t)t0 * p.ldx, min(TM, p.M - t0), p.ldx, p.K);
+    const bool gather = gathered(p);
+    const __amdgpu_buffer_rsrc_t rx = rows_rsrc(reinterpret_cast<const uint16_t *>(p.x) + (gather ? 0 : (size_t)t0 * p.ldx),
+                                                gather ? x_rows(p) : min(TM, p.M - t0), p.ldx, p.K);
     // copies: pieces of 8 rows; the wave takes pieces wv + NW j of the
     // stage's, so that copy j is of the same rows' matrix for every wave
     const int l8 = lane >> 3;
@@ -690,7 +1024,7 @@ __global__ __launch_bounds__(WN * WT * 64) void k_linear_tile(LinearParams p, in
         const int pc = wv + G::NW * j;
         const bool isx = G::NW * j >= TN / 8;
         const int row = (isx ? pc - TN / 8 : pc % (TN / 16)) * 8 + l8;
-        cv[j] = (uint32_t)(row * (isx ? p.ldx : p.ldw) * 2) + (kc + s0 * 64) * 2;
+        cv[j] = (ANY ? 0 : isx ? x_row(p, t0, row) : (uint32_t)(row * p.ldw * 2)) + (kc + s0 * 64) * 2;
     }
     // copy j of a stage (the next one in turn for that j) into a slot; checked where the stage may end past K or s1
     auto copy = [&](auto check, int stage, int slot, int j) {
@@ -702,17 +1036,44 @@ __global__ __launch_bounds__(WN * WT * 64) void k_linear_tile(LinearParams p, in
         else if (G::NW * j < TN / 16) copy16(r0, at, v);
         else copy16(r1, at, v);
     };
+    // MXFP4: the scales of rows 32 wv .. of the stage's (weight halves, tokens),
+    // two dwords a row
+    const int srow = (wv * 32 % (wv * 32 < TN ? TN / 2 : TN)) + (lane >> 1), sh = (lane & 1) * 4;
+    __amdgpu_buffer_rsrc_t rs = rx;
+    uint32_t sv = 0;
+    if constexpr (P::mx) {
+        const int blocks = ((p.K >> 3) + 3) & ~3;
+        if (wv * 32 < TN) {
+            const int nh = wv * 32 < TN / 2 ? n0 : n1, rows = min(TN / 2, p.N - nh);
+            const uint8_t *base = GATED && wv * 32 >= TN / 2 ? p.us : p.ws;
+            rs = grsrc(base + (size_t)(rows > 0 ? nh : 0) * p.ldws, rows > 0 ? (uint32_t)((rows - 1) * p.ldws + blocks) : 0u);
+            sv = (uint32_t)(srow * p.ldws) + sh + s0 * 8;
+        } else {
+            const int rows = gather ? x_rows(p) : min(TM, p.M - t0);
+            rs = grsrc(p.xs + (gather ? 0 : (size_t)t0 * p.ldxs), (uint32_t)((rows - 1) * p.ldxs + blocks));
+            const int r = gather ? x_source(p, t0 + srow) : srow;
+            sv = (wv * 32 - TN < TM && r >= 0 ? (uint32_t)(r * p.ldxs) : 0x80000000u) + sh + s0 * 8;
+        }
+    }
+    auto copy_scales = [&](int stage, int slot) {  // the next stage in turn
+        const uint32_t at = (uint32_t)(uintptr_t)lds + slot * G::STAGE + G::CODES + wv * 256;
+        copy4(rs, at, stage * 8 + sh < p.K >> 3 && stage < s1 ? sv : 0x80000000u);
+        sv += 8;
+    };
     // ANY: rows that direct copies cannot take (they want 16-byte pieces) go
     // through registers, loaded two stages before they are stored; rows past
     // the end repeat the last one, and their sums are not written
     const uint16_t *rp[G::CW];
+    bool there[G::CW];  // a gathered row without a source is zeros
     uint4 held[2][G::CW];
 #pragma unroll
     for (int j = 0; ANY && j < G::CW; j++) {
         const int pc = wv + G::NW * j, half = G::NW * j >= TN / 16;
-        if (G::NW * j >= TN / 8)
-            rp[j] = reinterpret_cast<const uint16_t *>(p.x) + (size_t)min(t0 + (pc - TN / 8) * 8 + l8, p.M - 1) * p.ldx;
-        else
+        if (G::NW * j >= TN / 8) {
+            const int t = min(t0 + (pc - TN / 8) * 8 + l8, p.M - 1), r = gather ? x_source(p, t) : t;
+            there[j] = r >= 0;
+            rp[j] = reinterpret_cast<const uint16_t *>(p.x) + (size_t)max(r, 0) * p.ldx;
+        } else
             rp[j] = (GATED && half ? U : W) + (size_t)min((half ? n1 : n0) + pc % (TN / 16) * 8 + l8, p.N - 1) * p.ldw;
     }
     auto load = [&](auto check, uint4(&h)[G::CW], int stage, int j) {
@@ -723,6 +1084,7 @@ __global__ __launch_bounds__(WN * WT * 64) void k_linear_tile(LinearParams p, in
             h[j] = make_uint4(0, 0, 0, 0);
             if (stage < s1) h[j] = load8(rp[j], k, p.K);
         }
+        if (P::grouped && G::NW * j >= TN / 8 && !there[j]) h[j] = make_uint4(0, 0, 0, 0);
     };
     auto store = [&](const uint4(&h)[G::CW], int slot, int j) {
         *reinterpret_cast<LDS u32x4_t *>(lds + wv * 1024 + slot * G::STAGE + G::NW * j * 1024 + lane * 16) =
@@ -740,9 +1102,16 @@ __global__ __launch_bounds__(WN * WT * 64) void k_linear_tile(LinearParams p, in
     constexpr int FA = 2 * G::FN, FT = G::FT, NM = FA * FT, NR = FA + FT;
     f32x4_t acc[FA][FT] = {};  // rows of half 0, then of half 1
     V a[2][FA], b[2][FT];
+    int sa[2][FA], sb[2][FT];  // MXFP4: the scales of these fragments, one per lane
     // read i (the token fragments first) of step st of a slot
     auto read = [&](int slot, int st, int i) {
         const LDS uint8_t *base = lds + slot * G::STAGE;
+        if constexpr (P::mx) {
+            const LDS uint8_t *s = base + G::CODES + r16 * 8 + st * 4 + q4;
+            const int f = i - FT;
+            if (i < FT) sb[st][i] = s[(TN + wt * (TM / WT) + i * 16) * 8];
+            else sa[st][f] = s[((f / G::FN) * (TN / 2) + wn * (TN / 2 / WN) + (f % G::FN) * 16) * 8];
+        }
         if (i < FT) {
             b[st][i] = __builtin_bit_cast(V, lds_ld16(base + fb[st] + i * 2048));
         } else {
@@ -756,12 +1125,14 @@ __global__ __launch_bounds__(WN * WT * 64) void k_linear_tile(LinearParams p, in
 #pragma unroll
         for (int i = 0; i < NM; i++) {
             const int f = i / FT, g = f & 1 ? FT - 1 - i % FT : i % FT;
-            acc[f][g] = mfma16v(a[st][f], b[st][g], acc[f][g]);
+            if constexpr (P::mx) acc[f][g] = mfma_mx(a[st][f], sa[st][f], b[st][g], sb[st][g], acc[f][g]);
+            else acc[f][g] = mfma16v(a[st][f], b[st][g], acc[f][g]);
 #pragma unroll
             for (int j = i * NR / NM; j < (i + 1) * NR / NM; j++) read(slot, 1 - st, j);
             if (!ANY && st == 1) {
 #pragma unroll
                 for (int j = i * G::CW / NM; j < (i + 1) * G::CW / NM; j++) copy(check, stage, into, j);
+                if (P::mx && i == NM - 1) copy_scales(stage, into);
             }
             __builtin_amdgcn_sched_barrier(0);
         }
@@ -785,8 +1156,11 @@ __global__ __launch_bounds__(WN * WT * 64) void k_linear_tile(LinearParams p, in
 #pragma unroll
         for (int i = 0; i < NST - 1; i++)
 #pragma unroll
-            for (int j = 0; j < G::CW; j++) copy(std::true_type{}, s0 + i, i, j);
-        wait_copies<(NST - 2) * G::CW>();
+            for (int j = 0; j < G::CALL; j++) {
+                if (j < G::CW) copy(std::true_type{}, s0 + i, i, j);
+                else copy_scales(s0 + i, i);
+            }
+        wait_copies<(NST - 2) * G::CALL>();
         barrier();
     }
 #pragma unroll
@@ -798,7 +1172,7 @@ __global__ __launch_bounds__(WN * WT * 64) void k_linear_tile(LinearParams p, in
         part(check, 0, slot, 0, 0);
         // (every wave has read the last stage's slot by now: it is filled anew below)
         if (ANY) lds_barrier();  // (loads into registers stay in flight across it)
-        else wait_copies<(NST - 3) * G::CW, 15>(), barrier();
+        else wait_copies<(NST - 3) * G::CALL, 15>(), barrier();
         __builtin_amdgcn_sched_barrier(0);
         part(check, 1, next, s + NST - 1, last);
         if (ANY) {
@@ -930,37 +1304,54 @@ __global__ __launch_bounds__(256) void k_linear_join(LinearParams p)
 // One stage more in the ring takes the same time.
 constexpr int kFewWaves = 8;
 
-template <bool GATED, int XP, int NST>
+template <bool GATED, int XP, int NST, bool MX>
 struct Few {
     static constexpr int NR = GATED ? 2 : 1, MT = (XP + 1) / 2;
-    static constexpr int CW = 2 * NR + XP, STAGE = CW * 1024;
+    static constexpr int CODES = (2 * NR + XP) * 1024;             // a stage's bytes, without the scales'
+    static constexpr int CW = 2 * NR + XP + (MX ? NR + 1 : 0), STAGE = CODES + (MX ? (NR + 1) * 256 : 0);
     static constexpr int RING = kFewWaves * NST * STAGE, JOIN = kFewWaves * NR * MT * 1024;
     static constexpr int LDSB = RING > JOIN ? RING : JOIN;
 };
 
-template <bool F16, bool GATED, int XP, int NST>
-__global__ __launch_bounds__(kFewWaves * 64) void k_linear_few(LinearParams p)
+template <bool F16, bool GATED, int XP, int NST, class P>
+__global__ __launch_bounds__(kFewWaves * 64) void k_linear_few(P p, int tn)
 {
-    using G = Few<GATED, XP, NST>;
+    using G = Few<GATED, XP, NST, P::mx>;
     using V = typename Frag<F16>::V;
     __shared__ __align__(1024) uint8_t lds_blk[G::LDSB];
     LDS uint8_t *lds = (LDS uint8_t *)lds_blk;
     const int lane = threadIdx.x & 63, wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int r16 = lane & 15, q4 = lane >> 4, l8 = lane >> 3;
-    const int n0 = blockIdx.x * 16, t0 = blockIdx.y * 8 * XP;
+    int ni = blockIdx.x, t0 = blockIdx.y * 8 * XP;
+    if (P::grouped && !block_tile<8 * XP>(p, tn, 0, t0, ni)) return;
+    const int n0 = ni * 16;
     const int SA = (p.K + 63) / 64, s0 = (int)((int64_t)SA * wv / kFewWaves), s1 = (int)((int64_t)SA * (wv + 1) / kFewWaves);
     const uint16_t *W = reinterpret_cast<const uint16_t *>(p.w), *U = reinterpret_cast<const uint16_t *>(p.w_up);
     const __amdgpu_buffer_rsrc_t rw = rows_rsrc(W + (size_t)n0 * p.ldw, min(16, p.N - n0), p.ldw, p.K);
     const __amdgpu_buffer_rsrc_t ru = GATED ? rows_rsrc(U + (size_t)n0 * p.ldw, min(16, p.N - n0), p.ldw, p.K) : rw;
-    const __amdgpu_buffer_rsrc_t rx =
-        rows_rsrc(reinterpret_cast<const uint16_t *>(p.x) + (size_t)t0 * p.ldx, min(8 * XP, p.M - t0), p.ldx, p.K);
+    const bool gather = gathered(p);
+    const __amdgpu_buffer_rsrc_t rx = rows_rsrc(reinterpret_cast<const uint16_t *>(p.x) + (gather ? 0 : (size_t)t0 * p.ldx),
+                                                gather ? x_rows(p) : min(8 * XP, p.M - t0), p.ldx, p.K);
     uint32_t cw[2], cx[XP];
     const int piece = (lane & 7) ^ (l8 >> 1);
     const int kc[2] = {piece * 8, (piece ^ 4) * 8};
 #pragma unroll
     for (int j = 0; j < 2; j++) cw[j] = (uint32_t)((8 * j + l8) * p.ldw * 2) + (kc[j] + s0 * 64) * 2;
 #pragma unroll
-    for (int j = 0; j < XP; j++) cx[j] = (uint32_t)((8 * j + l8) * p.ldx * 2) + (kc[j & 1] + s0 * 64) * 2;
+    for (int j = 0; j < XP; j++) cx[j] = x_row(p, t0, 8 * j + l8) + (kc[j & 1] + s0 * 64) * 2;
+    // MXFP4: the scales of 16 rows of each matrix and of the tokens, two dwords a row
+    __amdgpu_buffer_rsrc_t rs[3] = {rw, rw, rw};
+    uint32_t sv[2];
+    const int sh = (lane & 1) * 4;
+    if constexpr (P::mx) {
+        const int blocks = ((p.K >> 3) + 3) & ~3, rows = min(16, p.N - n0), xr = gather ? x_rows(p) : min(8 * XP, p.M - t0);
+        rs[0] = grsrc(p.ws + (size_t)n0 * p.ldws, (uint32_t)((rows - 1) * p.ldws + blocks));
+        if (GATED) rs[1] = grsrc(p.us + (size_t)n0 * p.ldws, (uint32_t)((rows - 1) * p.ldws + blocks));
+        rs[2] = grsrc(p.xs + (gather ? 0 : (size_t)t0 * p.ldxs), (uint32_t)((xr - 1) * p.ldxs + blocks));
+        const int r = lane >> 1, src = gather ? x_source(p, t0 + r) : r;
+        sv[0] = (r < 16 ? (uint32_t)(r * p.ldws) : 0x80000000u) + sh + s0 * 8;
+        sv[1] = (r < 8 * XP && src >= 0 ? (uint32_t)(src * p.ldxs) : 0x80000000u) + sh + s0 * 8;
+    }
     LDS uint8_t *ring = lds + wv * NST * G::STAGE;
     const uint32_t mring = (uint32_t)(uintptr_t)ring;
     auto copies = [&](int stage, int slot) {  // the next stage in turn
@@ -978,6 +1369,14 @@ __global__ __launch_bounds__(kFewWaves * 64) void k_linear_few(LinearParams p)
             copy16(rx, at + (2 * G::NR + j) * 1024, ok[j & 1] ? cx[j] : 0x80000000u);
             cx[j] += 128;
         }
+        if constexpr (P::mx) {
+            const bool in_k = in && stage * 8 + sh < p.K >> 3;
+#pragma unroll
+            for (int i = 0; i < G::NR; i++) copy4(rs[i], at + G::CODES + i * 256, in_k ? sv[0] : 0x80000000u);
+            copy4(rs[2], at + G::CODES + G::NR * 256, in_k ? sv[1] : 0x80000000u);
+            sv[0] += 8;
+            sv[1] += 8;
+        }
     };
     int fo[2];
 #pragma unroll
@@ -992,8 +1391,16 @@ __global__ __launch_bounds__(kFewWaves * 64) void k_linear_few(LinearParams p)
         wait_copies<(NST - 1) * G::CW>();
         const LDS uint8_t *base = ring + slot * G::STAGE;
         V a[2][G::NR], b[2][G::MT];
+        int sa[2][G::NR], sb[2][G::MT];
 #pragma unroll
         for (int st = 0; st < 2; st++) {
+            if constexpr (P::mx) {
+                const LDS uint8_t *s = base + G::CODES + r16 * 8 + st * 4 + q4;
+#pragma unroll
+                for (int i = 0; i < G::NR; i++) sa[st][i] = s[i * 256];
+#pragma unroll
+                for (int m = 0; m < G::MT; m++) sb[st][m] = (XP == 1 ? s - (r16 & 8) * 8 : s)[G::NR * 256 + m * 128];
+            }
 #pragma unroll
             for (int i = 0; i < G::NR; i++) a[st][i] = __builtin_bit_cast(V, lds_ld16(base + fo[st] + i * 2048));
 #pragma unroll
@@ -1007,7 +1414,10 @@ __global__ __launch_bounds__(kFewWaves * 64) void k_linear_few(LinearParams p)
 #pragma unroll
             for (int i = 0; i < G::NR; i++)
 #pragma unroll
-                for (int m = 0; m < G::MT; m++) acc[i][m] = mfma16v(a[st][i], b[st][m], acc[i][m]);
+                for (int m = 0; m < G::MT; m++) {
+                    if constexpr (P::mx) acc[i][m] = mfma_mx(a[st][i], sa[st][i], b[st][m], sb[st][m], acc[i][m]);
+                    else acc[i][m] = mfma16v(a[st][i], b[st][m], acc[i][m]);
+                }
         slot = slot + 1 == NST ? 0 : slot + 1;
     }
     wait_copies<0>();
@@ -1051,51 +1461,65 @@ void launch_join(const LinearParams &p, int ksplit, hipStream_t st)
     else if (ksplit == 8) k_linear_join<F16, GATED, 8><<<grid, 256, 0, st>>>(p);
 }
 
-template <bool F16, bool GATED, int XP, int NST>
-void launch_few(const LinearParams &p, hipStream_t st)
+// the most tiles of `rows` rows that the groups of p can make
+template <class P>
+int row_tiles(const P &p, int rows)
 {
-    const dim3 grid((p.N + 15) / 16, (p.M + 8 * XP - 1) / (8 * XP));
-    k_linear_few<F16, GATED, XP, NST><<<grid, kFewWaves * 64, 0, st>>>(p);
+    if constexpr (P::grouped) return (int)((p.M + (int64_t)std::min(p.groups, p.M) * (rows - 1)) / rows);
+    return (p.M + rows - 1) / rows;
 }
 
-template <bool F16, bool GATED, bool ANY, int TN, int TM, int WN, int WT, int NST>
-void launch_tile(const LinearParams &p, int ksplit, hipStream_t st)
+template <bool F16, bool GATED, int XP, int NST, class P>
+void launch_few(const P &p, hipStream_t st)
+{
+    const int tn = (p.N + 15) / 16, tt = row_tiles(p, 8 * XP);
+    const dim3 grid(P::grouped ? tn * tt : tn, P::grouped ? 1 : tt);
+    k_linear_few<F16, GATED, XP, NST><<<grid, kFewWaves * 64, 0, st>>>(p, tn);
+}
+
+template <bool F16, bool GATED, bool ANY, int TN, int TM, int WN, int WT, int NST, class P>
+void launch_tile(const P &p, int ksplit, hipStream_t st)
 {
     constexpr int NB = GATED ? TN / 2 : TN;
-    const int tt = (p.M + TM - 1) / TM, tn = (p.N + NB - 1) / NB;
+    const int tt = row_tiles(p, TM), tn = (p.N + NB - 1) / NB;
     k_linear_tile<F16, GATED, ANY, TN, TM, WN, WT, NST><<<tn * tt * ksplit, WN * WT * 64, 0, st>>>(p, tn, tt, ksplit);
-    launch_join<F16, GATED>(p, ksplit, st);
+    if constexpr (!P::grouped) launch_join<F16, GATED>(p, ksplit, st);
 }
 
-template <bool F16, bool GATED>
-void launch_big(const LinearParams &p, int ksplit, hipStream_t st)
+template <bool F16, bool GATED, class P>
+void launch_big(const P &p, int ksplit, hipStream_t st)
 {
     constexpr int NB = GATED ? 128 : 256;
-    const int tt = (p.M + 255) / 256, tn = (p.N + NB - 1) / NB;
-    k_linear_big<F16, GATED><<<tn * tt * ksplit, 256, 0, st>>>(p, tn, tt, ksplit);
-    launch_join<F16, GATED>(p, ksplit, st);
+    const int tt = row_tiles(p, 256), tn = (p.N + NB - 1) / NB;
+    if constexpr (P::mx) k_mx_big<F16, GATED><<<tn * tt * ksplit, 256, 0, st>>>(p, tn, tt, ksplit);
+    else k_linear_big<F16, GATED><<<tn * tt * ksplit, 256, 0, st>>>(p, tn, tt, ksplit);
+    if constexpr (!P::grouped) launch_join<F16, GATED>(p, ksplit, st);
 }
 
-template <bool F16, bool GATED>
-void launch_gated(const LinearParams &p, const LinearPlan &c, hipStream_t st)
+template <bool F16, bool GATED, class P>
+void launch_gated(const P &p, const LinearPlan &c, hipStream_t st)
 {
     switch (c.kind) {
     case kFew1: return launch_few<F16, GATED, 1, GATED ? 2 : 3>(p, st);
     case kFew2: return launch_few<F16, GATED, 2, 2>(p, st);
     case kFew4: return launch_few<F16, GATED, 4, 2>(p, st);
     case kTile64x32: return launch_tile<F16, GATED, false, 64, 32, 2, 2, 6>(p, c.ksplit, st);
-    case kTile64x64: return launch_tile<F16, GATED, false, 64, 64, 2, 2, 5>(p, c.ksplit, st);
+    case kTile64x64: return launch_tile<F16, GATED, false, 64, 64, 2, 2, P::mx ? 4 : 5>(p, c.ksplit, st);
     case kTile128x64: return launch_tile<F16, GATED, false, 128, 64, 4, 2, 6>(p, c.ksplit, st);
     case kTile128x128: return launch_tile<F16, GATED, false, 128, 128, 2, 4, 4>(p, c.ksplit, st);
-    case kAny64x32: return launch_tile<F16, GATED, true, 64, 32, 2, 2, 3>(p, c.ksplit, st);
-    case kAny64x64: return launch_tile<F16, GATED, true, 64, 64, 2, 2, 3>(p, c.ksplit, st);
-    case kAny128x128: return launch_tile<F16, GATED, true, 128, 128, 2, 4, 3>(p, c.ksplit, st);
     case kBig: return launch_big<F16, GATED>(p, c.ksplit, st);
+    }
+    if constexpr (!P::mx) {
+        switch (c.kind) {
+        case kAny64x32: return launch_tile<F16, GATED, true, 64, 32, 2, 2, 3>(p, c.ksplit, st);
+        case kAny64x64: return launch_tile<F16, GATED, true, 64, 64, 2, 2, 3>(p, c.ksplit, st);
+        case kAny128x128: return launch_tile<F16, GATED, true, 128, 128, 2, 4, 3>(p, c.ksplit, st);
+        }
     }
 }
 
-template <bool F16>
-void launch_typed(const LinearParams &p, const LinearPlan &c, hipStream_t st)
+template <bool F16, class P>
+void launch_typed(const P &p, const LinearPlan &c, hipStream_t st)
 {
     if (p.w_up) launch_gated<F16, true>(p, c, st);
     else launch_gated<F16, false>(p, c, st);

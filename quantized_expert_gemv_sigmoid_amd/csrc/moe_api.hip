@@ -526,6 +526,157 @@ moe_status check_linear(const moe_linear_desc *d)
     return MOE_OK;
 }
 
+bool finite_betas(int32_t act, float b1, float b2)
+{
+    return act != MOE_LINEAR_SITU_GLU || (isfinite(b1) && isfinite(b2) && b1 > 0 && b2 > 0);
+}
+
+// what moe_mx_linear_desc and moe_grouped_desc have alike
+template <class Desc>
+moe_status check_product(const Desc *d)
+{
+    if (d->n_in < 1 || d->n_out < 1) return MOE_EINVAL;
+    if (d->type != MOE_BF16 && d->type != MOE_F16) return MOE_EINVAL;
+    if (d->act < MOE_LINEAR_NONE || d->act > MOE_LINEAR_SWIGLU) return MOE_EINVAL;
+    if (!finite_betas(d->act, d->situ_b1, d->situ_b2)) return MOE_EINVAL;
+    if (d->bias_type != MOE_F32 && d->bias_type != d->type) return MOE_EINVAL;
+    const bool gated = linear_gated(d->act);
+    if (!d->w || gated != (d->w_up != nullptr) || (!gated && d->bias_up)) return MOE_EINVAL;
+    const size_t ba = d->bias_type == MOE_F32 ? 4 : 2;
+    if (!aligned(d->bias, ba) || !aligned(d->bias_up, ba)) return MOE_EINVAL;
+    if (d->n_in > kMaxLinear || d->n_out > kMaxLinear) return MOE_EUNSUPPORTED;
+    return MOE_OK;
+}
+
+template <class Desc>
+void fill_product(const Desc *d, moe::LinearParams &p)
+{
+    p.N = d->n_out;
+    p.act = d->act;
+    p.b1 = d->situ_b1;
+    p.b2 = d->situ_b2;
+    p.w = d->w;
+    p.w_up = d->w_up;
+    p.bias = d->bias;
+    p.bias_up = d->bias_up;
+    p.bias_f32 = d->bias_type == MOE_F32;
+}
+
+// rows of codes: whole blocks, at multiples of 16 bytes
+constexpr int64_t kMaxCodeLd = 2 * kMaxLd;
+bool code_rows(int64_t ld, int32_t n_in) { return ld >= n_in / 2 && ld % 16 == 0; }
+
+moe_status check_mx_linear(const moe_mx_linear_desc *d)
+{
+    if (!d) return MOE_EINVAL;
+    const moe_status st = check_product(d);
+    if (st == MOE_EINVAL) return st;
+    if (d->n_in % 32 || !code_rows(d->ldw, d->n_in) || d->ldw_s < d->n_in / 32) return MOE_EINVAL;
+    if (d->residual_type != MOE_F32 && d->residual_type != d->type) return MOE_EINVAL;
+    if (!d->w_s || linear_gated(d->act) != (d->w_up_s != nullptr)) return MOE_EINVAL;
+    if (!aligned(d->w, 16) || !aligned(d->w_up, 16)) return MOE_EINVAL;
+    if (st != MOE_OK || d->ldw > kMaxCodeLd || d->ldw_s > kMaxLd) return MOE_EUNSUPPORTED;
+    return MOE_OK;
+}
+
+moe::MxParams mx_params(const moe_mx_linear_desc *d, int32_t T)
+{
+    moe::MxParams p = {};
+    fill_product(d, p);
+    p.M = T;
+    p.K = d->n_in / 4;
+    p.ldw = d->ldw / 2;
+    p.ws = d->w_s;
+    p.us = d->w_up_s;
+    p.ldws = d->ldw_s;
+    p.res_f32 = d->residual_type == MOE_F32;
+    return p;
+}
+
+moe_status check_grouped(const moe_grouped_desc *d)
+{
+    if (!d) return MOE_EINVAL;
+    const moe_status st = check_product(d);
+    if (st == MOE_EINVAL) return st;
+    if (d->n_groups < 1) return MOE_EINVAL;
+    if (d->operands == MOE_MXFP4) {
+        if (d->n_in % 32 || !code_rows(d->ldw, d->n_in) || d->ldw_s < d->n_in / 32) return MOE_EINVAL;
+        if (d->group_w % 16 || !aligned(d->w, 16) || !aligned(d->w_up, 16)) return MOE_EINVAL;
+        if (!d->w_s || linear_gated(d->act) != (d->w_up_s != nullptr)) return MOE_EINVAL;
+        if (d->n_in % 128 || d->ldw_s % 4 || d->group_w_s % 4 || !aligned(d->w_s, 4) || !aligned(d->w_up_s, 4))
+            return MOE_EUNSUPPORTED;
+        if (d->ldw > kMaxCodeLd || d->ldw_s > kMaxLd) return MOE_EUNSUPPORTED;
+        if (d->group_w_s < 0) return MOE_EINVAL;
+    } else {
+        if (d->operands != d->type || d->ldw < d->n_in || !aligned(d->w, 2) || !aligned(d->w_up, 2)) return MOE_EINVAL;
+        if (d->ldw > kMaxLd) return MOE_EUNSUPPORTED;
+    }
+    if (d->group_w < 0) return MOE_EINVAL;
+    if (st != MOE_OK || d->n_groups > moe::kMaxExperts) return MOE_EUNSUPPORTED;
+    return MOE_OK;
+}
+
+constexpr int32_t kMaxGroupedRows = 1 << 24;
+
+// checks of a call of R >= 1 rows, and its parameters
+moe_status grouped_params(const moe_grouped_desc *d, const void *x, const uint8_t *x_s, int64_t ldx, int64_t ldxs, int32_t x_rows,
+                          const int32_t *rows, const int32_t *offsets, int32_t R, moe::GroupedMxParams &p)
+{
+    const bool mx = d->operands == MOE_MXFP4;
+    if (x_rows < 1 || (!rows && x_rows < R) || !offsets || !x) return MOE_EINVAL;
+    if (!aligned(rows, 4) || !aligned(offsets, 4)) return MOE_EINVAL;
+    const int units = mx ? d->n_in / 4 : d->n_in;  // of 16 bits in a row
+    if (mx) {
+        if (x_rows == 1) {
+            ldx = d->n_in / 2;
+            ldxs = d->n_in / 32;
+        }
+        if (!code_rows(ldx, d->n_in) || ldxs < d->n_in / 32 || !aligned(x, 16) || !x_s) return MOE_EINVAL;
+        if (ldxs % 4 || !aligned(x_s, 4) || ldx > kMaxCodeLd || ldxs > kMaxLd) return MOE_EUNSUPPORTED;
+        ldx /= 2;
+    } else {
+        if (x_rows == 1) ldx = d->n_in;
+        if (ldx < d->n_in || !aligned(x, 2) || x_s) return MOE_EINVAL;
+        if (ldx > kMaxLd) return MOE_EUNSUPPORTED;
+    }
+    // (gathered rows are found by 32-bit offsets from the first)
+    const int64_t far = (int64_t)1 << 31;
+    if (rows && (((int64_t)(x_rows - 1) * ldx + units) * 2 > far || (mx && x_rows * ldxs > far))) return MOE_EUNSUPPORTED;
+    fill_product(d, p);
+    p.M = R;
+    p.K = units;
+    p.x = x;
+    p.ldx = ldx;
+    p.ldw = mx ? d->ldw / 2 : d->ldw;
+    p.wstride = mx ? d->group_w / 2 : d->group_w;
+    p.bstride = d->n_out;
+    p.offsets = offsets;
+    p.rows = rows;
+    p.groups = d->n_groups;
+    p.xrows = x_rows;
+    p.xs = x_s;
+    p.ws = d->w_s;
+    p.us = d->w_up_s;
+    p.ldxs = ldxs;
+    p.ldws = d->ldw_s;
+    p.sstride = d->group_w_s;
+    return MOE_OK;
+}
+
+bool value_type(int32_t t) { return t == MOE_BF16 || t == MOE_F16 || t == MOE_F32; }
+size_t value_size(int32_t t) { return t == MOE_F32 ? 4 : 2; }
+
+moe_status check_mx_rows(const void *v, int32_t type, int64_t ld, int32_t T, int32_t cols, const uint8_t *codes, int64_t ldc,
+                         const uint8_t *scales, int64_t lds)
+{
+    if (!value_type(type) || T < 0 || cols < 1) return MOE_EINVAL;
+    if (cols > kMaxLinear) return MOE_EUNSUPPORTED;
+    const int64_t blocks = (cols + 31) / 32;
+    if (T > 1 && (ld < cols || ldc < 16 * blocks || lds < blocks)) return MOE_EINVAL;
+    if (T > 0 && (!v || !codes || !scales || !aligned(v, value_size(type)))) return MOE_EINVAL;
+    return MOE_OK;
+}
+
 moe::LinearParams linear_params(const moe_linear_desc *d, int32_t T)
 {
     moe::LinearParams p = {};
@@ -812,6 +963,180 @@ moe_status moe_linear(const moe_linear_desc *desc, const void *x, int64_t ldx, i
     p.ldo = ldo;
     p.part = (float *)ws;
     MOE_TRY(moe::launch_linear(p, desc->type == MOE_F16, (hipStream_t)stream));
+    return MOE_OK;
+}
+
+moe_status moe_mx_quantize(const void *x, int32_t type, int64_t ldx, int32_t T, int32_t n, int32_t rule, uint8_t *codes,
+                           int64_t ldc, uint8_t *scales, int64_t lds, void *stream)
+{
+    if (rule != MOE_MX_FLOOR && rule != MOE_MX_FIT) return MOE_EINVAL;
+    const moe_status st = check_mx_rows(x, type, ldx, T, n, codes, ldc, scales, lds);
+    if (st != MOE_OK || T == 0) return st;
+    (void)hipGetLastError();
+    MOE_TRY(moe::launch_mx_quantize(x, type, ldx, T, n, codes, ldc, scales, lds, rule == MOE_MX_FIT, (hipStream_t)stream));
+    return MOE_OK;
+}
+
+moe_status moe_mx_dequantize(const uint8_t *codes, int64_t ldc, const uint8_t *scales, int64_t lds, int32_t T, int32_t n, void *out,
+                             int32_t type, int64_t ldo, void *stream)
+{
+    const moe_status st = check_mx_rows(out, type, ldo, T, n, codes, ldc, scales, lds);
+    if (st != MOE_OK || T == 0) return st;
+    (void)hipGetLastError();
+    MOE_TRY(moe::launch_mx_dequantize(codes, ldc, scales, lds, T, n, out, type, ldo, (hipStream_t)stream));
+    return MOE_OK;
+}
+
+size_t moe_mx_linear_workspace_bytes(const moe_mx_linear_desc *desc, int32_t max_tokens)
+{
+    if (check_mx_linear(desc) != MOE_OK || max_tokens < 0 || max_tokens > kMaxTokens) return 0;
+    return moe::mx_linear_workspace(mx_params(desc, max_tokens));
+}
+
+int32_t moe_mx_linear_path_for(const moe_mx_linear_desc *desc, int32_t T)
+{
+    const moe_status st = check_mx_linear(desc);
+    if (st != MOE_OK) return st;
+    if (T < 1) return MOE_EINVAL;
+    if (T > kMaxTokens) return MOE_EUNSUPPORTED;
+    const moe::LinearPlan c = moe::mx_linear_plan(mx_params(desc, T));
+    return c.kind + 256 * c.ksplit;
+}
+
+moe_status moe_mx_linear(const moe_mx_linear_desc *desc, const uint8_t *x, int64_t ldx, const uint8_t *x_s, int64_t ldxs, int32_t T,
+                         const void *residual, int64_t ldr, void *out_half, float *out_f32, int64_t ldo, int32_t out_mode,
+                         void *ws, size_t ws_bytes, void *stream)
+{
+    const moe_status st = check_mx_linear(desc);
+    if (st != MOE_OK) return st;
+    if (T < 0) return MOE_EINVAL;
+    if (T == 1) {  // (no second row: whatever its distance)
+        ldx = desc->n_in / 2;
+        ldxs = desc->n_in / 32;
+        ldo = desc->n_out;
+        if (residual) ldr = desc->n_out;
+    }
+    if (!code_rows(ldx, desc->n_in) || ldxs < desc->n_in / 32 || ldo < desc->n_out) return MOE_EINVAL;
+    if (residual && ldr != 0 && ldr < desc->n_out) return MOE_EINVAL;
+    if (out_mode != MOE_OUT_BF16 && out_mode != MOE_OUT_F32 && out_mode != MOE_OUT_BOTH) return MOE_EINVAL;
+    if (T > kMaxTokens || ldx > kMaxCodeLd || ldxs > kMaxLd || ldo > kMaxLd || (residual && ldr > kMaxLd)) return MOE_EUNSUPPORTED;
+    if (T == 0) return MOE_OK;
+    if (!x || !aligned(x, 16) || !x_s) return MOE_EINVAL;
+    if (residual && !aligned(residual, value_size(desc->residual_type))) return MOE_EINVAL;
+    if (out_mode != MOE_OUT_F32 && (!out_half || !aligned(out_half, 2))) return MOE_EINVAL;
+    if (out_mode != MOE_OUT_BF16 && (!out_f32 || !aligned(out_f32, 4))) return MOE_EINVAL;
+    if (!ws || !aligned(ws, 256)) return MOE_EINVAL;
+    moe::MxParams p = mx_params(desc, T);
+    if (ws_bytes < moe::mx_linear_workspace(p)) return MOE_EWORKSPACE;
+    (void)hipGetLastError();
+    p.x = x;
+    p.ldx = ldx / 2;
+    p.xs = x_s;
+    p.ldxs = ldxs;
+    p.res = residual;
+    p.ldr = ldr;
+    p.out_half = out_mode != MOE_OUT_F32 ? out_half : nullptr;
+    p.out_f32 = out_mode != MOE_OUT_BF16 ? out_f32 : nullptr;
+    p.ldo = ldo;
+    p.part = (float *)ws;
+    MOE_TRY(moe::launch_mx_linear(p, desc->type == MOE_F16, (hipStream_t)stream));
+    return MOE_OK;
+}
+
+int32_t moe_grouped_path_for(const moe_grouped_desc *desc, const void *x, int64_t ldx, int32_t R)
+{
+    const moe_status st = check_grouped(desc);
+    if (st != MOE_OK) return st;
+    if (R < 1 || !x) return MOE_EINVAL;
+    if (R > kMaxGroupedRows) return MOE_EUNSUPPORTED;
+    moe::GroupedMxParams p = {};
+    const int32_t offsets = 0;
+    // (scales: any aligned address, none is read)
+    const uint8_t *xs = desc->operands == MOE_MXFP4 ? reinterpret_cast<const uint8_t *>(&offsets) : nullptr;
+    const moe_status s2 = grouped_params(desc, x, xs, ldx, desc->n_in / 32, R, nullptr, &offsets, R, p);
+    if (s2 != MOE_OK) return s2;
+    const moe::LinearPlan c = moe::grouped_plan(p, desc->operands == MOE_MXFP4);
+    return c.kind + 256 * c.ksplit;
+}
+
+moe_status moe_grouped_linear(const moe_grouped_desc *desc, const void *x, int64_t ldx, const uint8_t *x_s, int64_t ldxs,
+                              int32_t x_rows, const int32_t *rows, const int32_t *offsets, int32_t R, void *out_half,
+                              float *out_f32, int64_t ldo, int32_t out_mode, void *stream)
+{
+    const moe_status st = check_grouped(desc);
+    if (st != MOE_OK) return st;
+    if (R < 0) return MOE_EINVAL;
+    if (R == 1) ldo = desc->n_out;
+    if (ldo < desc->n_out) return MOE_EINVAL;
+    if (out_mode != MOE_OUT_BF16 && out_mode != MOE_OUT_F32 && out_mode != MOE_OUT_BOTH) return MOE_EINVAL;
+    if (R > kMaxGroupedRows || ldo > kMaxLd) return MOE_EUNSUPPORTED;
+    if (R == 0) return MOE_OK;
+    if (out_mode != MOE_OUT_F32 && (!out_half || !aligned(out_half, 2))) return MOE_EINVAL;
+    if (out_mode != MOE_OUT_BF16 && (!out_f32 || !aligned(out_f32, 4))) return MOE_EINVAL;
+    moe::GroupedMxParams p = {};
+    const moe_status s2 = grouped_params(desc, x, x_s, ldx, ldxs, x_rows, rows, offsets, R, p);
+    if (s2 != MOE_OK) return s2;
+    p.out_half = out_mode != MOE_OUT_F32 ? out_half : nullptr;
+    p.out_f32 = out_mode != MOE_OUT_BF16 ? out_f32 : nullptr;
+    p.ldo = ldo;
+    (void)hipGetLastError();
+    if (desc->operands == MOE_MXFP4) MOE_TRY(moe::launch_grouped_mx(p, desc->type == MOE_F16, (hipStream_t)stream));
+    else MOE_TRY(moe::launch_grouped(p, desc->type == MOE_F16, (hipStream_t)stream));
+    return MOE_OK;
+}
+
+size_t moe_group_workspace_bytes(int32_t max_tokens, int32_t top_k, int32_t n_experts)
+{
+    if (max_tokens < 0 || max_tokens > kMaxTokens || top_k < 1 || top_k > moe::kMaxTopK) return 0;
+    if (n_experts < 1 || n_experts > moe::kMaxExperts) return 0;
+    return moe::group_workspace((int64_t)max_tokens * top_k, n_experts);
+}
+
+moe_status moe_group(const int32_t *ids, int32_t T, int32_t top_k, int32_t n_experts, int32_t *offsets, int32_t *tokens,
+                     int32_t *places, void *ws, size_t ws_bytes, void *stream)
+{
+    if (T < 0 || top_k < 1 || n_experts < 1) return MOE_EINVAL;
+    if (T > kMaxTokens || top_k > moe::kMaxTopK || n_experts > moe::kMaxExperts) return MOE_EUNSUPPORTED;
+    if (!offsets || !aligned(offsets, 4)) return MOE_EINVAL;
+    if (T > 0 && (!ids || !tokens || !places || !aligned(ids, 4) || !aligned(tokens, 4) || !aligned(places, 4))) return MOE_EINVAL;
+    if (!ws || !aligned(ws, 256)) return MOE_EINVAL;
+    const int64_t R = (int64_t)T * top_k;
+    if (ws_bytes < moe::group_workspace(R, n_experts)) return MOE_EWORKSPACE;
+    (void)hipGetLastError();
+    MOE_TRY(moe::launch_group(ids, R, top_k, n_experts, offsets, tokens, places, ws, (hipStream_t)stream));
+    return MOE_OK;
+}
+
+moe_status moe_combine(const void *y, int32_t y_type, int64_t ldy, int32_t R, const int32_t *places, const float *weights, int32_t T,
+                       int32_t top_k, int32_t n, const void *residual, int32_t residual_type, int64_t ldr, void *out,
+                       int32_t out_type, int64_t ldo, void *stream)
+{
+    if (T < 0 || R < 0 || top_k < 1 || n < 1) return MOE_EINVAL;
+    if (!value_type(y_type) || !value_type(out_type) || (residual && !value_type(residual_type))) return MOE_EINVAL;
+    if (T > kMaxTokens || top_k > moe::kMaxTopK || n > kMaxLinear) return MOE_EUNSUPPORTED;
+    if ((R > 1 && ldy < n) || (T > 1 && ldo < n) || (T > 1 && residual && ldr != 0 && ldr < n)) return MOE_EINVAL;
+    if (T == 0) return MOE_OK;
+    if (!places || !out || (R > 0 && !y)) return MOE_EINVAL;
+    if (!aligned(places, 4) || !aligned(weights, 4) || !aligned(y, value_size(y_type)) || !aligned(out, value_size(out_type)))
+        return MOE_EINVAL;
+    if (residual && !aligned(residual, value_size(residual_type))) return MOE_EINVAL;
+    moe::CombineParams p = {};
+    p.y = y;
+    p.res = residual;
+    p.places = places;
+    p.weights = weights;
+    p.out = out;
+    p.ldy = ldy;
+    p.ldr = ldr;
+    p.ldo = ldo;
+    p.T = T;
+    p.k = top_k;
+    p.n = n;
+    p.rows = R;
+    p.res_type = residual_type;
+    p.out_type = out_type;
+    (void)hipGetLastError();
+    MOE_TRY(moe::launch_group_combine(p, y_type, (hipStream_t)stream));
     return MOE_OK;
 }
 
