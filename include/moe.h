@@ -411,11 +411,12 @@ size_t moe_linear_workspace_bytes(const moe_linear_desc *desc, int32_t max_token
  * is split into; a negative moe_status for a call it refuses.  Launches
  * nothing and reads nothing behind the pointers.  ROWS16: 16 weight rows a
  * block and 8, 16 or 32 tokens; TILE, ANY: weight rows x tokens, ANY where
- * rows of x or w are not 16-byte aligned. */
+ * rows of x or w are not 16-byte aligned (TILE256X128: of moe_mx_linear and
+ * moe_grouped_linear only). */
 typedef enum {
     MOE_LINEAR_ROWS16X8 = 0, MOE_LINEAR_ROWS16X16 = 1, MOE_LINEAR_ROWS16X32 = 2, MOE_LINEAR_TILE64X32 = 3,
     MOE_LINEAR_TILE64X64 = 4, MOE_LINEAR_TILE128X64 = 5, MOE_LINEAR_TILE128X128 = 6, MOE_LINEAR_ANY64X32 = 7,
-    MOE_LINEAR_ANY64X64 = 8, MOE_LINEAR_ANY128X128 = 9, MOE_LINEAR_TILE256X256 = 10
+    MOE_LINEAR_ANY64X64 = 8, MOE_LINEAR_ANY128X128 = 9, MOE_LINEAR_TILE256X256 = 10, MOE_LINEAR_TILE256X128 = 11
 } moe_linear_path;
 int32_t moe_linear_path_for(const moe_linear_desc *desc, const void *x, int64_t ldx, int32_t T);
 

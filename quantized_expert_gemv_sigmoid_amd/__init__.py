@@ -29,7 +29,8 @@ GROUP_MAX, GROUP_TOP2 = 0, 1
 (LINEAR_NONE, LINEAR_RELU, LINEAR_SILU, LINEAR_GELU, LINEAR_GELU_TANH, LINEAR_SITU_GLU,
  LINEAR_SWIGLU) = range(7)
 (LINEAR_ROWS16X8, LINEAR_ROWS16X16, LINEAR_ROWS16X32, LINEAR_TILE64X32, LINEAR_TILE64X64, LINEAR_TILE128X64,
- LINEAR_TILE128X128, LINEAR_ANY64X32, LINEAR_ANY64X64, LINEAR_ANY128X128, LINEAR_TILE256X256) = range(11)
+ LINEAR_TILE128X128, LINEAR_ANY64X32, LINEAR_ANY64X64, LINEAR_ANY128X128, LINEAR_TILE256X256,
+ LINEAR_TILE256X128) = range(12)
 
 EXPORTS = ("moe_workspace_bytes", "moe_path_for", "moe_route", "moe_expert_forward",
            "moe_layer", "moe_layer_noalloc", "moe_layer_timed", "moe_set_one_token_router_wait",

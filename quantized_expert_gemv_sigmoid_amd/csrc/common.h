@@ -581,7 +581,7 @@ using GroupedMxParams = MxOf<GroupedParams>;
 // which kernel a product takes, and into how many parts of K it is split
 // (the numbers of moe_linear_path)
 enum LinearKind {
-    kFew1, kFew2, kFew4, kTile64x32, kTile64x64, kTile128x64, kTile128x128, kAny64x32, kAny64x64, kAny128x128, kBig
+    kFew1, kFew2, kFew4, kTile64x32, kTile64x64, kTile128x64, kTile128x128, kAny64x32, kAny64x64, kAny128x128, kBig, kTile256x128
 };
 struct LinearPlan {
     int kind, ksplit;

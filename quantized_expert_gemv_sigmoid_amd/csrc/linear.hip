@@ -52,6 +52,7 @@ constexpr Kind kKinds[] = {
     {kTile128x64, 128, 64, 0, 320, false, true, false, 5500.0},
     {kTile128x128, 128, 128, 0, 470, false, true, false, 5500.0},
     {kBig, 256, 256, 0, 1270, false, true, false, 5500.0},
+    {kTile256x128, 256, 128, 0, 800, true, true, false, 5500.0},
     {kAny64x32, 64, 32, 170, 345, true, true, true, 5500.0},
     {kAny64x64, 64, 64, 200, 400, true, true, true, 5500.0},
     {kAny128x128, 128, 128, 0, 890, false, true, true, 5500.0},
@@ -72,14 +73,14 @@ constexpr Kind kKinds[] = {
 // 1117 x 2049 64 x 64 19.1, 128 x 128 19.9; 333 x 3585 x 3587 128 x 128 in two
 // parts 30.8, 64 x 64 in two 38.5; 4096 x 3584 x 7168 256 x 256 165, 128 x 128
 // 246; 9 x 3584 x 7168 16 x 16 10.4, 64 x 32 11.3.
-LinearPlan plan(const LinearParams &p, bool any)
+LinearPlan plan(const LinearParams &p, bool any, bool mx = false)
 {
     const int m = p.w_up ? 2 : 1, stages = (p.K + 63) / 64;
     const double weights = 2.0 * m * p.N * p.K;
     LinearPlan best = {any ? kAny64x64 : kTile64x64, 1};
     double least = 1e30;
     for (const Kind &k : kKinds) {
-        if (k.any != any) continue;
+        if (k.any != any || (k.kind == kTile256x128 && !mx)) continue;
         const double tiles = (double)((p.N * (int64_t)m + k.rows - 1) / k.rows) * ((p.M + k.tokens - 1) / k.tokens);
         for (int ks = 1; ks <= (k.split ? kMaxSplit : 1); ks *= 2) {
             if (ks > 1 && (stages < 4 * ks || tiles * ks > 4 * kCus || part_bytes(p, ks) > kPartBytes)) break;
@@ -133,7 +134,7 @@ size_t x_scales(const MxParams &p) { return up256((size_t)p.M * scale_pitch(p));
 size_t mx_linear_workspace(const MxParams &p) { return up256(linear_workspace(p)) + weight_scales(p) + x_scales(p); }
 
 // A stage of 256 codes takes the bytes, reads and cycles of a 16-bit one of 64
-LinearPlan mx_linear_plan(const MxParams &p) { return plan(p, false); }
+LinearPlan mx_linear_plan(const MxParams &p) { return plan(p, false, true); }
 
 hipError_t launch_mx_linear(const MxParams &params, bool f16, hipStream_t st)
 {
@@ -165,25 +166,42 @@ hipError_t launch_mx_linear(const MxParams &params, bool f16, hipStream_t st)
 
 // -------------------------------------------------------------------- groups
 
+namespace {
+
+// A kernel's tile, and the time in ns of a stage of 64 of K (256 of codes) and
+// of a block's start and end, per block and CU.
+struct GroupedKind {
+    int kind, rows, tokens, each_ns, ends_ns;
+    bool any;
+};
+constexpr GroupedKind kGroupedKinds[] = {
+    {kTile64x32, 64, 32, 130, 2350, false},    {kTile64x64, 64, 64, 180, 2750, false},
+    {kTile128x64, 128, 64, 310, 4500, false},  {kTile128x128, 128, 128, 500, 6000, false},
+    {kTile256x128, 256, 128, 950, 5000, false}, {kAny64x32, 64, 32, 400, 2500, true},
+    {kAny64x64, 64, 64, 500, 3000, true},      {kAny128x128, 128, 128, 950, 6500, true},
+};
+
+}  // namespace
+
 // plan()'s estimate where the rows of each group are not known: as if the M
 // rows fell on the groups at random, which leaves some of them empty where
-// there are few rows, and a tile of each other group half full on average.
+// there are few rows, and a tile of each other group half full on average; and
+// with the ends of a block, since a group's product is often a short one.
 LinearPlan grouped_plan(const GroupedParams &p, bool mx)
 {
     const bool any = !mx && !(pieces(p) && p.wstride % 8 == 0);
     const int m = p.w_up ? 2 : 1, stages = (p.K + 63) / 64;
     const double active = p.groups * (1.0 - std::exp(-(double)p.M / p.groups));
     const double weights = 2.0 * m * active * p.N * p.K;
-    LinearPlan best = {any ? kAny128x128 : kBig, 1};
+    LinearPlan best = {any ? kAny128x128 : kTile256x128, 1};
     double least = 1e30;
-    for (const Kind &k : kKinds) {
+    for (const GroupedKind &k : kGroupedKinds) {
         if (k.any != any) continue;
         const double columns = std::ceil((double)p.N * m / k.rows);
         if (columns * ((double)p.M / k.tokens + p.groups) > 1e9) continue;
-        const double tiles = columns * std::max(active, (double)p.M / k.tokens + 0.5 * active);
-        const double full = tiles / kCus, each = k.shared ? std::max(1.0, full) : std::ceil(full);
-        const double work = (k.base_ns + each * k.each_ns) * stages;
-        const double ns = std::max(work, weights / k.rate) + 0.1 * work;
+        const double full = columns * std::max(active, (double)p.M / k.tokens + 0.5 * active) / kCus;
+        const double work = std::max(1.0, full) * k.each_ns * stages + full * k.ends_ns;
+        const double ns = std::max(work, weights / 5600.0) + 0.1 * work;
         if (ns < least) {
             least = ns;
             best = {k.kind, 1};

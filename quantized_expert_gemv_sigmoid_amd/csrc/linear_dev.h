@@ -274,6 +274,7 @@ __device__ __forceinline__ void barrier()
 }
 
 typedef uint32_t u32x2_t __attribute__((ext_vector_type(2)));
+typedef uint16_t u16x2_t __attribute__((ext_vector_type(2)));
 
 template <bool F16>
 struct Frag {
@@ -385,6 +386,12 @@ __device__ __forceinline__ bool block_tile(P &p, int tn, int tt, int &t0, int &n
 }
 
 template <class P>
+__device__ __forceinline__ int group_start(const P &p, int g)
+{
+    return min(max(p.offsets[min(g, p.groups)], 0), p.M);
+}
+
+template <class P>
 __device__ __forceinline__ bool gathered(const P &p)
 {
     if constexpr (P::grouped) return p.rows != nullptr;
@@ -420,8 +427,8 @@ __device__ __forceinline__ uint32_t x_row(const P &p, int t0, int row)
 
 // The end of a 256 x 256 tile: a wave's sums acc[A half][B half][16 n][16
 // tokens] to the outputs (ks of ksplit: to the partial sums).
-template <bool F16, bool GATED, class P>
-__device__ __forceinline__ void finish_big(const P &p, LDS uint8_t *lds, const f32x4_t (&acc)[2][2][4][4], int t0, int n0, int ks,
+template <bool F16, bool GATED>
+__device__ __forceinline__ void finish_big(const LinearParams &p, LDS uint8_t *lds, const f32x4_t (&acc)[2][2][4][4], int t0, int n0, int ks,
                                            int ksplit)
 {
     const int lane = threadIdx.x & 63, wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -580,40 +587,39 @@ __device__ __forceinline__ void finish_big(const P &p, LDS uint8_t *lds, const f
 // give way to power.  The rest is the last
 // turn of tiles (448 on 256 CUs) and the epilogue, which nothing overlaps as
 // a CU holds one block.
-template <bool F16, bool GATED, class P>
-__global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(1, 1))) void k_linear_big(P p, int tn, int tt, int ksplit)
+template <bool F16, bool GATED>
+__global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(1, 1))) void k_linear_big(LinearParams p, int tn,
+                                                                                               int tt, int ksplit)
 {
     using V = typename Frag<F16>::V;
     __shared__ __align__(1024) uint8_t lds_blk[kBigLds];
     LDS uint8_t *lds = (LDS uint8_t *)lds_blk;
     const int lane = threadIdx.x & 63, wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    int t0, ni;
-    if (!block_tile<256>(p, tn, tt, t0, ni)) return;
-    const int n0 = ni * (GATED ? 128 : 256);
+    int ti, ni;
+    tile_of(blockIdx.x % (tn * tt), tn, tt, ni, ti);
+    const int t0 = ti * 256, n0 = ni * (GATED ? 128 : 256);
     // the block's part of K
-    const int ks = P::grouped ? 0 : blockIdx.x / (tn * tt), SA = (p.K + 63) / 64;
+    const int ks = blockIdx.x / (tn * tt), SA = (p.K + 63) / 64;
     const int kb = (int)((int64_t)SA * ks / ksplit) * 64, K = min(p.K, (int)((int64_t)SA * (ks + 1) / ksplit) * 64) - kb;
     const uint16_t *W = reinterpret_cast<const uint16_t *>(p.w) + kb, *U = reinterpret_cast<const uint16_t *>(p.w_up) + kb;
-    const bool gather = gathered(p);
-    const uint16_t *X = reinterpret_cast<const uint16_t *>(p.x) + kb + (gather ? 0 : (size_t)t0 * p.ldx);
+    const uint16_t *X = reinterpret_cast<const uint16_t *>(p.x) + kb + (size_t)t0 * p.ldx;
     const int na1 = n0 + 128;
     const __amdgpu_buffer_rsrc_t rA0 = rows_rsrc(W + (size_t)n0 * p.ldw, min(128, p.N - n0), p.ldw, K);
     const __amdgpu_buffer_rsrc_t rA1 =
         GATED ? rows_rsrc(U + (size_t)n0 * p.ldw, min(128, p.N - n0), p.ldw, K)
               : rows_rsrc(na1 < p.N ? W + (size_t)na1 * p.ldw : W, min(128, p.N - na1), p.ldw, K);
-    const __amdgpu_buffer_rsrc_t rB0 = rows_rsrc(X, gather ? x_rows(p) : min(128, p.M - t0), p.ldx, K);
+    const __amdgpu_buffer_rsrc_t rB0 = rows_rsrc(X, min(128, p.M - t0), p.ldx, K);
     const __amdgpu_buffer_rsrc_t rB1 =
-        gather ? rB0 : rows_rsrc(t0 + 128 < p.M ? X + (size_t)128 * p.ldx : X, min(128, p.M - t0 - 128), p.ldx, K);
+        rows_rsrc(t0 + 128 < p.M ? X + (size_t)128 * p.ldx : X, min(128, p.M - t0 - 128), p.ldx, K);
 
     // copies: the wave's 32 rows of a unit in four pieces of 8, this lane's 16 bytes of each
     const int l8 = lane >> 3, piece = (lane & 7) ^ (l8 >> 1);
-    uint32_t va[4], vb[4], vg[4];  // vg: of the second half of gathered rows
+    uint32_t va[4], vb[4];
 #pragma unroll
     for (int j = 0; j < 4; j++) {
         const uint32_t row = 32 * wv + 8 * j + l8, col = (piece ^ (j & 1 ? 4 : 0)) * 16;
         va[j] = (uint32_t)(row * p.ldw * 2) + col;
-        vb[j] = x_row(p, t0, row) + col;
-        if (P::grouped) vg[j] = (gather ? x_row(p, t0, row + 128) : (uint32_t)(row * p.ldx * 2)) + col;
+        vb[j] = (uint32_t)(row * p.ldx * 2) + col;
     }
     int kc0 = piece * 8, kc1 = (piece ^ 4) * 8;
     const uint32_t m0w = (uint32_t)(uintptr_t)lds + wv * 4096;
@@ -622,7 +628,7 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(1, 1))) voi
     // piece j of the wave's part of a unit, D stages on (checked where that stage may end past K)
     auto copy = [&](auto check, auto d, __amdgpu_buffer_rsrc_t r, int at, bool b, int j) {
         constexpr int D = decltype(d)::value;
-        uint32_t v = (b ? (P::grouped && (at == B1 || at == BUF + B1) ? vg[j] : vb[j]) : va[j]) + D * 128;
+        uint32_t v = (b ? vb[j] : va[j]) + D * 128;
         if (decltype(check)::value) v = (j & 1 ? kc1 : kc0) + D * 64 < K ? v : 0x80000000u;
         copy16(r, m0w + at + j * 1024, v);
     };
@@ -706,10 +712,7 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(1, 1))) voi
         turn(fb, -BUF);
         phase(check, D3{}, rA1, BUF + A1, false, acc[1][1], a1, b1, [&](int i) { readB(b0, B0, i); });
 #pragma unroll
-        for (int j = 0; j < 4; j++) {
-            va[j] += 256, vb[j] += 256;
-            if (P::grouped) vg[j] += 256;
-        }
+        for (int j = 0; j < 4; j++) va[j] += 256, vb[j] += 256;
         kc0 += 128;
         kc1 += 128;
     };
@@ -753,54 +756,46 @@ constexpr int kMxLds = 4 * kBigWave > 8 * kMxUnit ? 4 * kBigWave : 8 * kMxUnit;
 // bytes of a row are 256 codes, and one product takes 128 of them in the
 // cycles of a 16-bit one's 32.  The 8 scales of a row and stage are copied
 // behind their unit; a lane's products take one byte each, read from there.
-template <bool F16, bool GATED, class P>
-__global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(1, 1))) void k_mx_big(P p, int tn, int tt, int ksplit)
+template <bool F16, bool GATED>
+__global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(1, 1))) void k_mx_big(MxParams p, int tn, int tt, int ksplit)
 {
     __shared__ __align__(1024) uint8_t lds_blk[kMxLds];
     LDS uint8_t *lds = (LDS uint8_t *)lds_blk;
     const int lane = threadIdx.x & 63, wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    int t0, ni;
-    if (!block_tile<256>(p, tn, tt, t0, ni)) return;
-    const int n0 = ni * (GATED ? 128 : 256);
-    const int ks = P::grouped ? 0 : blockIdx.x / (tn * tt), SA = (p.K + 63) / 64;
+    int ti, ni;
+    tile_of(blockIdx.x % (tn * tt), tn, tt, ni, ti);
+    const int t0 = ti * 256, n0 = ni * (GATED ? 128 : 256);
+    const int ks = blockIdx.x / (tn * tt), SA = (p.K + 63) / 64;
     const int kb = (int)((int64_t)SA * ks / ksplit) * 64, K = min(p.K, (int)((int64_t)SA * (ks + 1) / ksplit) * 64) - kb;
     const uint16_t *W = reinterpret_cast<const uint16_t *>(p.w) + kb, *U = reinterpret_cast<const uint16_t *>(p.w_up) + kb;
-    const bool gather = gathered(p);
-    const uint16_t *X = reinterpret_cast<const uint16_t *>(p.x) + kb + (gather ? 0 : (size_t)t0 * p.ldx);
-    const uint8_t *WS = p.ws + (kb >> 3), *US = GATED ? p.us + (kb >> 3) : nullptr;
-    const uint8_t *XS = p.xs + (kb >> 3) + (gather ? 0 : (size_t)t0 * p.ldxs);
-    const int na1 = GATED ? n0 : n0 + 128, ra0 = min(128, p.N - n0), ra1 = min(128, p.N - na1), at1 = ra1 > 0 ? na1 : 0;
-    const int xr = x_rows(p), rb0 = gather ? xr : min(128, p.M - t0), rb1 = gather ? xr : min(128, p.M - t0 - 128);
-    const int bt1 = gather || rb1 <= 0 ? 0 : 128;
+    const uint16_t *X = reinterpret_cast<const uint16_t *>(p.x) + kb + (size_t)t0 * p.ldx;
+    const uint8_t *WS = p.ws + (kb >> 3), *US = GATED ? p.us + (kb >> 3) : WS, *XS = p.xs + (kb >> 3) + (size_t)t0 * p.ldxs;
+    const int n1 = GATED ? n0 : n0 + 128, na0 = min(128, p.N - n0), na1 = min(128, p.N - n1), m1 = na1 > 0 ? n1 : 0;
+    const int nb0 = min(128, p.M - t0), nb1 = min(128, p.M - t0 - 128), x1 = nb1 > 0 ? 128 : 0;
     auto scales_rsrc = [&](const uint8_t *base, int rows, int64_t ld) {
         return grsrc(base, rows > 0 ? (uint32_t)((rows - 1) * ld + (((K >> 3) + 3) & ~3)) : 0u);
     };
-    const __amdgpu_buffer_rsrc_t rA0 = rows_rsrc(W + (size_t)n0 * p.ldw, ra0, p.ldw, K);
-    const __amdgpu_buffer_rsrc_t rA1 = rows_rsrc((GATED ? U : W) + (size_t)at1 * p.ldw, ra1, p.ldw, K);
-    const __amdgpu_buffer_rsrc_t rB0 = rows_rsrc(X, rb0, p.ldx, K);
-    const __amdgpu_buffer_rsrc_t rB1 = rows_rsrc(X + (size_t)bt1 * p.ldx, rb1, p.ldx, K);
-    const __amdgpu_buffer_rsrc_t sA0 = scales_rsrc(WS + (size_t)n0 * p.ldws, ra0, p.ldws);
-    const __amdgpu_buffer_rsrc_t sA1 = scales_rsrc((GATED ? US : WS) + (size_t)at1 * p.ldws, ra1, p.ldws);
-    const __amdgpu_buffer_rsrc_t sB0 = scales_rsrc(XS, rb0, p.ldxs);
-    const __amdgpu_buffer_rsrc_t sB1 = scales_rsrc(XS + (size_t)bt1 * p.ldxs, rb1, p.ldxs);
+    const __amdgpu_buffer_rsrc_t rA0 = rows_rsrc(W + (size_t)n0 * p.ldw, na0, p.ldw, K);
+    const __amdgpu_buffer_rsrc_t rA1 = rows_rsrc((GATED ? U : W) + (size_t)m1 * p.ldw, na1, p.ldw, K);
+    const __amdgpu_buffer_rsrc_t rB0 = rows_rsrc(X, nb0, p.ldx, K);
+    const __amdgpu_buffer_rsrc_t rB1 = rows_rsrc(X + (size_t)x1 * p.ldx, nb1, p.ldx, K);
+    const __amdgpu_buffer_rsrc_t sA0 = scales_rsrc(WS + (size_t)n0 * p.ldws, na0, p.ldws);
+    const __amdgpu_buffer_rsrc_t sA1 = scales_rsrc(US + (size_t)m1 * p.ldws, na1, p.ldws);
+    const __amdgpu_buffer_rsrc_t sB0 = scales_rsrc(XS, nb0, p.ldxs);
+    const __amdgpu_buffer_rsrc_t sB1 = scales_rsrc(XS + (size_t)x1 * p.ldxs, nb1, p.ldxs);
 
     // copies: the wave's 32 rows of a unit in four pieces of 8, this lane's 16
     // bytes of each, and half a row's scales
     const int l8 = lane >> 3, piece = (lane & 7) ^ (l8 >> 1);
-    uint32_t va[4], vb[4], vg[4];
+    uint32_t va[4], vb[4];
 #pragma unroll
     for (int j = 0; j < 4; j++) {
         const uint32_t row = 32 * wv + 8 * j + l8, col = (piece ^ (j & 1 ? 4 : 0)) * 16;
         va[j] = (uint32_t)(row * p.ldw * 2) + col;
-        vb[j] = x_row(p, t0, row) + col;
-        if (P::grouped) vg[j] = (gather ? x_row(p, t0, row + 128) : (uint32_t)(row * p.ldx * 2)) + col;
+        vb[j] = (uint32_t)(row * p.ldx * 2) + col;
     }
     const int srow = 32 * wv + (lane >> 1), sh = (lane & 1) * 4;
-    auto scale_row = [&](int row) {
-        const int r = gather ? x_source(p, t0 + row) : srow;
-        return (r < 0 ? 0x80000000u : (uint32_t)(r * p.ldxs)) + sh;
-    };
-    uint32_t vas = (uint32_t)(srow * p.ldws) + sh, vbs = scale_row(srow), vgs = P::grouped ? scale_row(srow + 128) : vbs;
+    uint32_t vas = (uint32_t)(srow * p.ldws) + sh, vbs = (uint32_t)(srow * p.ldxs) + sh;
     int kc0 = piece * 8, kc1 = (piece ^ 4) * 8, kcs = sh * 8;
     const uint32_t m0w = (uint32_t)(uintptr_t)lds + wv * 4096, m0s = (uint32_t)(uintptr_t)lds + kUnit + wv * 256;
     constexpr int A0 = 0, A1 = kMxUnit, B0 = 2 * kMxUnit, B1 = 3 * kMxUnit, BUF = 4 * kMxUnit;
@@ -808,13 +803,12 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(1, 1))) voi
     // (checked where that stage may end past K)
     auto copy = [&](auto check, auto d, __amdgpu_buffer_rsrc_t r, __amdgpu_buffer_rsrc_t s, int at, bool b, int j) {
         constexpr int D = decltype(d)::value;
-        const bool second = P::grouped && (at == B1 || at == BUF + B1);
         if (j < 4) {
-            uint32_t v = (b ? (second ? vg[j] : vb[j]) : va[j]) + D * 128;
+            uint32_t v = (b ? vb[j] : va[j]) + D * 128;
             if (decltype(check)::value) v = (j & 1 ? kc1 : kc0) + D * 64 < K ? v : 0x80000000u;
             copy16(r, m0w + at + j * 1024, v);
         } else {
-            uint32_t v = (b ? (second ? vgs : vbs) : vas) + D * 8;
+            uint32_t v = (b ? vbs : vas) + D * 8;
             if (decltype(check)::value) v = kcs + D * 64 < K ? v : 0x80000000u;
             copy4(s, m0s + at, v);
         }
@@ -904,11 +898,8 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(1, 1))) voi
         turn(fb, -BUF);
         phase(check, D3{}, rA1, sA1, BUF + A1, false, acc[1][1], a1, b1, [&](int i) { readB(b0, B0, i); });
 #pragma unroll
-        for (int j = 0; j < 4; j++) {
-            va[j] += 256, vb[j] += 256;
-            if (P::grouped) vg[j] += 256;
-        }
-        vas += 16, vbs += 16, vgs += 16;
+        for (int j = 0; j < 4; j++) va[j] += 256, vb[j] += 256;
+        vas += 16, vbs += 16;
         kc0 += 128;
         kc1 += 128;
         kcs += 128;
@@ -1292,6 +1283,246 @@ __global__ __launch_bounds__(256) void k_linear_join(LinearParams p)
     finish_row<F16, GATED>(p, t[0], n, a, u);
 }
 
+// ------------------------------------------------- groups, two blocks to a CU
+
+// 256 x 128 outputs (gated: 128 of each matrix) per block, four waves of 128 x
+// 64 whose 128 sums per lane leave room for a second block on the CU: one's
+// first copies, activations and stores run beside the other's products.  K in
+// stages of 128 bytes a row; a stage's weights come in four quarters of 64 rows
+// (32 for either pair of waves), each multiplied with the whole stage's tokens
+// in a phase of its own: quarters in a ring of five, tokens in one of two.
+template <bool MX>
+struct Pair {
+    static constexpr int QROWS = 64, TOKENS = 128, NA = 5, NB = 2;
+    static constexpr int QCODES = QROWS * 128, A = QCODES + (MX ? QROWS * 8 : 0);
+    static constexpr int BCODES = TOKENS * 128, B = BCODES + (MX ? TOKENS * 8 : 0);
+    static constexpr int B0 = NA * A, PAD = B0 + NB * B, RING = PAD + (MX ? 256 : 0);
+    static constexpr int C = MX ? 4 : 3;  // copies per wave and phase
+    static constexpr int EROW = 64 * 4 + 16, EWAVE = 2 * 32 * EROW;  // epilogue: two halves of 32 tokens
+    static constexpr int LDSB = RING > 4 * EWAVE ? RING : 4 * EWAVE;
+    static_assert(LDSB <= 80 * 1024, "two blocks to a CU");
+};
+
+template <bool F16, bool GATED, class P>
+__global__ __launch_bounds__(256, 2) void k_linear_pair(P p, int tn, int tt, int ksplit)
+{
+    using G = Pair<P::mx>;
+    using V = typename Frag<F16>::V;
+    __shared__ __align__(1024) uint8_t lds_blk[G::LDSB];
+    LDS uint8_t *lds = (LDS uint8_t *)lds_blk;
+    const int lane = threadIdx.x & 63, wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    int t0, ni;
+    if (!block_tile<G::TOKENS>(p, tn, tt, t0, ni)) return;
+    const int n0 = ni * (GATED ? 128 : 256), n1 = GATED ? n0 : n0 + 128;
+    const int ks = P::grouped ? 0 : blockIdx.x / (tn * tt), SA = (p.K + 63) / 64;
+    const int kb = (int)((int64_t)SA * ks / ksplit) * 64, K = min(p.K, (int)((int64_t)SA * (ks + 1) / ksplit) * 64) - kb;
+    const uint16_t *W = reinterpret_cast<const uint16_t *>(p.w) + kb, *U = reinterpret_cast<const uint16_t *>(p.w_up) + kb;
+    const bool gather = gathered(p);
+    const int h0 = min(128, p.N - n0), h1 = min(128, p.N - n1), nh1 = h1 > 0 ? n1 : 0;
+    const int xr = gather ? x_rows(p) : min(G::TOKENS, p.M - t0);
+    const __amdgpu_buffer_rsrc_t r0 = rows_rsrc(W + (size_t)n0 * p.ldw, h0, p.ldw, K);
+    const __amdgpu_buffer_rsrc_t r1 = rows_rsrc((GATED ? U : W) + (size_t)nh1 * p.ldw, h1, p.ldw, K);
+    const __amdgpu_buffer_rsrc_t rx =
+        rows_rsrc(reinterpret_cast<const uint16_t *>(p.x) + kb + (gather ? 0 : (size_t)t0 * p.ldx), xr, p.ldx, K);
+
+    // copies: 16 rows of a weight quarter per wave (rows 16 wv + 8 j + lane / 8
+    // of it: half a quarter each for either pair of waves), 8 of the tokens' next 32
+    const int l8 = lane >> 3, piece = (lane & 7) ^ (l8 >> 1);
+    const int ka[2] = {piece * 8, (piece ^ 4) * 8}, kx = (piece ^ (wv & 1 ? 4 : 0)) * 8;
+    uint32_t va[2], vx[4];
+#pragma unroll
+    for (int j = 0; j < 2; j++) {
+        const int i = 16 * wv + 8 * j + l8;
+        va[j] = (uint32_t)(((i >> 5) * 64 + (i & 31)) * p.ldw * 2) + ka[j] * 2;
+    }
+#pragma unroll
+    for (int j = 0; j < 4; j++) vx[j] = x_row(p, t0, 32 * j + 8 * wv + l8) + kx * 2;
+    const uint32_t d32 = (uint32_t)(32 * p.ldw * 2);
+    const uint32_t base = (uint32_t)(uintptr_t)lds;
+    // MXFP4: two dwords of scales a row, by waves 0 and 1 the quarter's, by
+    // wave 2 the tokens'; wave 3 copies zeros past the ring.  vs[q]: beside
+    // quarter q of the weights, whose phase copies rows 32 ((q + 2) % 4) .. of
+    // the tokens; ss: of its two halves, or the tokens'
+    __amdgpu_buffer_rsrc_t ss[2] = {rx, rx};
+    uint32_t vs[4] = {};
+    const int sh = (lane & 1) * 4;
+    if constexpr (P::mx) {
+        const int blocks = ((K >> 3) + 3) & ~3;
+        auto scales = [&](const uint8_t *q, int rows, int64_t ld) {
+            return grsrc(q + (kb >> 3), rows > 0 ? (uint32_t)((rows - 1) * ld + blocks) : 0u);
+        };
+        if (wv < 2) {
+            ss[0] = scales(p.ws + (size_t)n0 * p.ldws, h0, p.ldws);
+            ss[1] = scales((GATED ? p.us : p.ws) + (size_t)nh1 * p.ldws, h1, p.ldws);
+        } else {
+            ss[0] = ss[1] = scales(p.xs + (gather ? 0 : (size_t)t0 * p.ldxs), xr, p.ldxs);
+        }
+#pragma unroll
+        for (int q = 0; q < 4; q++) {
+            const int xrow = 32 * ((q + 2) & 3) + (lane >> 1), src = gather ? x_source(p, t0 + xrow) : xrow;
+            const int wrow = wv * 64 + 32 * (q & 1) + (lane >> 1);
+            const int64_t at = wv < 2 ? wrow * p.ldws : wv == 2 && src >= 0 ? src * p.ldxs : 0x80000000ll;
+            vs[q] = (uint32_t)at + sh;
+        }
+    }
+    // copy i of C: two of quarter q of stage `stage` into slot `slot`, (where x)
+    // rows 32 ((q + 2) % 4) .. of stage xstage's tokens, and (MXFP4) the scales
+    auto copy = [&](int i, int q, int stage, int slot, bool x, int xstage) {
+        const uint32_t at = base + slot * G::A, xat = base + G::B0 + (xstage & 1) * G::B;
+        const int j = (q + 2) & 3;
+        if (i < 2) {
+            const uint32_t v = va[i] + (q & 1 ? d32 : 0u) + stage * 128;
+            copy16(q & 2 ? r1 : r0, at + wv * 2048 + i * 1024, stage * 64 + ka[i] < K ? v : 0x80000000u);
+        } else if (i == 2) {
+            if (x) copy16(rx, xat + j * 4096 + wv * 1024, xstage * 64 + kx < K ? vx[j] + xstage * 128 : 0x80000000u);
+        } else {
+            const int st = wv < 2 ? stage : x ? xstage : K;
+            const uint32_t to = wv < 2 ? at + G::QCODES + wv * 256 : wv == 2 && x ? xat + G::BCODES + j * 256 : base + G::PAD;
+            copy4(ss[q >> 1], to, st * 64 + sh * 8 < K ? vs[q] + st * 8 : 0x80000000u);
+        }
+    };
+    auto copies = [&](int q, int stage, int slot, bool x, int xstage) {
+#pragma unroll
+        for (int i = 0; i < G::C; i++) copy(i, q, stage, slot, x, xstage);
+    };
+
+    const int r16 = lane & 15, q4 = lane >> 4;
+    const int wn = wv >> 1, wt = wv & 1;
+    int fo[2];
+#pragma unroll
+    for (int st = 0; st < 2; st++) fo[st] = r16 * 128 + (((st * 4 + q4) ^ (r16 >> 1)) << 4);
+    const LDS uint8_t *fa = lds + wn * 4096, *fb = lds + G::B0 + wt * 8192;
+    const int fsa = G::QCODES + (wn * 32 + r16) * 8 + q4, fsb = G::BCODES + (wt * 64 + r16) * 8 + q4;
+    f32x4_t acc[4][2][4] = {};  // [quarter][16 rows][16 tokens]
+    V a[2][2][2], b[2][4];      // [buffer][step][16 rows], [step][16 tokens]
+    int sa[2][2][2], sb[2][4];
+    auto read_a = [&](int buf, int slot) {
+#pragma unroll
+        for (int st = 0; st < 2; st++)
+#pragma unroll
+            for (int f = 0; f < 2; f++) {
+                if constexpr (P::mx) sa[buf][st][f] = lds[slot * G::A + fsa + f * 128 + st * 4];
+                a[buf][st][f] = __builtin_bit_cast(V, lds_ld16(fa + slot * G::A + fo[st] + f * 2048));
+            }
+    };
+    auto read_b = [&](int slot) {
+#pragma unroll
+        for (int st = 0; st < 2; st++)
+#pragma unroll
+            for (int g = 0; g < 4; g++) {
+                if constexpr (P::mx) sb[st][g] = lds[G::B0 + slot * G::B + fsb + g * 128 + st * 4];
+                b[st][g] = __builtin_bit_cast(V, lds_ld16(fb + slot * G::B + fo[st] + g * 2048));
+            }
+    };
+    // Phase n = 4 s + q copies quarter n + 5 (into the slot that the phase
+    // before it read) and a fourth of the tokens of stage s + 2 (s + 1 while q
+    // is 0: their slot was read in phase 4 s), so what a phase reads was copied
+    // four phases before at least.
+    auto first = [&](int q) {  // the tokens beside quarter q, of stage 0
+        const int j = (q + 2) & 3;
+        copy16(rx, base + G::B0 + j * 4096 + wv * 1024, kx < K ? vx[j] : 0x80000000u);
+        if constexpr (P::mx) {
+            const bool on = wv == 2 && sh * 8 < K;
+            copy4(ss[0], base + (wv == 2 ? G::B0 + G::BCODES + j * 256 : G::PAD), on ? vs[q] : 0x80000000u);
+        }
+    };
+    first(1);
+    first(2);
+    first(3);
+    copies(0, 0, 0, true, 0);
+    copies(1, 0, 1, false, 0);
+    copies(2, 0, 2, true, 1);
+    copies(3, 0, 3, true, 1);
+    copies(0, 1, 4, true, 1);
+    wait_copies<4 * G::C - 1>();
+    barrier();
+    read_a(0, 0);
+    int slot = 0;  // of the quarter that is multiplied
+    const int S = (K + 63) / 64;
+    for (int s = 0; s < S; s++) {
+#pragma unroll
+        for (int q = 0; q < 4; q++) {
+            const int next = slot + 1 == G::NA ? 0 : slot + 1;
+            __builtin_amdgcn_sched_barrier(0);
+            wait_copies<3 * G::C>();
+            barrier();
+            __builtin_amdgcn_sched_barrier(0);
+            if (q == 0) read_b(s & 1);
+            read_a((q + 1) & 1, next);
+            // (the copies between the products: a wave waits at a copy while the
+            // memory pipeline is taken)
+#pragma unroll
+            for (int i = 0; i < 16; i++) {
+                const int st = i >> 3, f = (i >> 2) & 1, g = f ? 3 - (i & 3) : i & 3;
+                if constexpr (P::mx)
+                    acc[q][f][g] = mfma_mx(a[q & 1][st][f], sa[q & 1][st][f], b[st][g], sb[st][g], acc[q][f][g]);
+                else acc[q][f][g] = mfma16v(a[q & 1][st][f], b[st][g], acc[q][f][g]);
+                __builtin_amdgcn_sched_barrier(0);
+                if (i % 4 == 1 && i / 4 < G::C)
+                    copy(i / 4, (q + 1) & 3, q == 3 ? s + 2 : s + 1, slot, true, q == 0 ? s + 1 : s + 2);
+                __builtin_amdgcn_sched_barrier(0);
+            }
+            slot = next;
+        }
+    }
+    __builtin_amdgcn_sched_barrier(0);
+    wait_copies<0>();
+    barrier();
+
+    // epilogue: 32 tokens of both halves at a time through the wave's own LDS,
+    // so that a row's 64 outputs leave as 16 lanes x 4
+    LDS uint8_t *buf = lds + wv * G::EWAVE;
+    constexpr int HALVES = GATED ? 1 : 2, R = 8;
+    const int c4 = (lane & 15) * 4;
+#pragma unroll
+    for (int round = 0; round < 2; round++) {
+#pragma unroll
+        for (int q = 0; q < 4; q++)
+#pragma unroll
+            for (int f = 0; f < 2; f++)
+#pragma unroll
+                for (int g = 0; g < 2; g++)
+                    *reinterpret_cast<LDS f32x4_t *>(buf + ((q >> 1) * 32 + g * 16 + r16) * G::EROW + ((q & 1) * 2 + f) * 64 + q4 * 16) =
+                        acc[q][f][round * 2 + g];
+#pragma unroll 1
+        for (int h = 0; h < HALVES; h++) {
+            const int n = (h ? n1 : n0) + wn * 64 + c4;
+            const LDS uint8_t *row = buf + (h * 32 + q4) * G::EROW + c4 * 4;
+            int t[R];
+#pragma unroll
+            for (int i = 0; i < R; i++) {
+                t[i] = t0 + wt * 64 + round * 32 + q4 + 4 * i;
+                t[i] = t[i] < p.M && n < p.N ? t[i] : -1;
+            }
+            auto sums = [&](int second, int i) {
+                return *reinterpret_cast<const LDS f32x4_t *>(row + (second * 32 + 4 * i) * G::EROW);
+            };
+            if (ksplit > 1) {
+#pragma unroll
+                for (int i = 0; i < R; i++)
+                    if (t[i] >= 0) store_part<GATED>(p, ks, t[i], n, sums(0, i), sums(GATED ? 1 : 0, i));
+                continue;
+            }
+            uint4 res[R] = {};
+            load_res<R>(p, t, n, res);
+            float v[4 * R], u[4 * R], ba[4], bu[4] = {};
+            bias4<F16>(p.bias, p.bias_f32, n, p.N, ba);
+            if (GATED) bias4<F16>(p.bias_up, p.bias_f32, n, p.N, bu);
+#pragma unroll
+            for (int i = 0; i < R; i++) {
+                const f32x4_t c = sums(0, i), d = sums(GATED ? 1 : 0, i);
+#pragma unroll
+                for (int j = 0; j < 4; j++) {
+                    v[4 * i + j] = c[j] + ba[j];
+                    u[4 * i + j] = GATED ? d[j] + bu[j] : 0.0f;
+                }
+            }
+            activate<GATED>(v, u, p.act, p.b1, p.b2);
+            write_rows<F16, R>(p, t, n, v, res);
+        }
+    }
+}
+
 // ------------------------------------------------------------ served batches
 
 // A block multiplies 16 weight rows (gated: 16 of each matrix) with 8 XP
@@ -1314,7 +1545,7 @@ struct Few {
 };
 
 template <bool F16, bool GATED, int XP, int NST, class P>
-__global__ __launch_bounds__(kFewWaves * 64) void k_linear_few(P p, int tn)
+__global__ __launch_bounds__(kFewWaves * 64) void k_linear_few(P p)
 {
     using G = Few<GATED, XP, NST, P::mx>;
     using V = typename Frag<F16>::V;
@@ -1322,35 +1553,32 @@ __global__ __launch_bounds__(kFewWaves * 64) void k_linear_few(P p, int tn)
     LDS uint8_t *lds = (LDS uint8_t *)lds_blk;
     const int lane = threadIdx.x & 63, wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int r16 = lane & 15, q4 = lane >> 4, l8 = lane >> 3;
-    int ni = blockIdx.x, t0 = blockIdx.y * 8 * XP;
-    if (P::grouped && !block_tile<8 * XP>(p, tn, 0, t0, ni)) return;
-    const int n0 = ni * 16;
+    const int n0 = blockIdx.x * 16, t0 = blockIdx.y * 8 * XP;
     const int SA = (p.K + 63) / 64, s0 = (int)((int64_t)SA * wv / kFewWaves), s1 = (int)((int64_t)SA * (wv + 1) / kFewWaves);
     const uint16_t *W = reinterpret_cast<const uint16_t *>(p.w), *U = reinterpret_cast<const uint16_t *>(p.w_up);
     const __amdgpu_buffer_rsrc_t rw = rows_rsrc(W + (size_t)n0 * p.ldw, min(16, p.N - n0), p.ldw, p.K);
     const __amdgpu_buffer_rsrc_t ru = GATED ? rows_rsrc(U + (size_t)n0 * p.ldw, min(16, p.N - n0), p.ldw, p.K) : rw;
-    const bool gather = gathered(p);
-    const __amdgpu_buffer_rsrc_t rx = rows_rsrc(reinterpret_cast<const uint16_t *>(p.x) + (gather ? 0 : (size_t)t0 * p.ldx),
-                                                gather ? x_rows(p) : min(8 * XP, p.M - t0), p.ldx, p.K);
+    const __amdgpu_buffer_rsrc_t rx =
+        rows_rsrc(reinterpret_cast<const uint16_t *>(p.x) + (size_t)t0 * p.ldx, min(8 * XP, p.M - t0), p.ldx, p.K);
     uint32_t cw[2], cx[XP];
     const int piece = (lane & 7) ^ (l8 >> 1);
     const int kc[2] = {piece * 8, (piece ^ 4) * 8};
 #pragma unroll
     for (int j = 0; j < 2; j++) cw[j] = (uint32_t)((8 * j + l8) * p.ldw * 2) + (kc[j] + s0 * 64) * 2;
 #pragma unroll
-    for (int j = 0; j < XP; j++) cx[j] = x_row(p, t0, 8 * j + l8) + (kc[j & 1] + s0 * 64) * 2;
+    for (int j = 0; j < XP; j++) cx[j] = (uint32_t)((8 * j + l8) * p.ldx * 2) + (kc[j & 1] + s0 * 64) * 2;
     // MXFP4: the scales of 16 rows of each matrix and of the tokens, two dwords a row
     __amdgpu_buffer_rsrc_t rs[3] = {rw, rw, rw};
     uint32_t sv[2];
     const int sh = (lane & 1) * 4;
     if constexpr (P::mx) {
-        const int blocks = ((p.K >> 3) + 3) & ~3, rows = min(16, p.N - n0), xr = gather ? x_rows(p) : min(8 * XP, p.M - t0);
+        const int blocks = ((p.K >> 3) + 3) & ~3, rows = min(16, p.N - n0), xr = min(8 * XP, p.M - t0);
         rs[0] = grsrc(p.ws + (size_t)n0 * p.ldws, (uint32_t)((rows - 1) * p.ldws + blocks));
         if (GATED) rs[1] = grsrc(p.us + (size_t)n0 * p.ldws, (uint32_t)((rows - 1) * p.ldws + blocks));
-        rs[2] = grsrc(p.xs + (gather ? 0 : (size_t)t0 * p.ldxs), (uint32_t)((xr - 1) * p.ldxs + blocks));
-        const int r = lane >> 1, src = gather ? x_source(p, t0 + r) : r;
+        rs[2] = grsrc(p.xs + (size_t)t0 * p.ldxs, (uint32_t)((xr - 1) * p.ldxs + blocks));
+        const int r = lane >> 1;
         sv[0] = (r < 16 ? (uint32_t)(r * p.ldws) : 0x80000000u) + sh + s0 * 8;
-        sv[1] = (r < 8 * XP && src >= 0 ? (uint32_t)(src * p.ldxs) : 0x80000000u) + sh + s0 * 8;
+        sv[1] = (r < 8 * XP ? (uint32_t)(r * p.ldxs) : 0x80000000u) + sh + s0 * 8;
     }
     LDS uint8_t *ring = lds + wv * NST * G::STAGE;
     const uint32_t mring = (uint32_t)(uintptr_t)ring;
@@ -1472,9 +1700,8 @@ int row_tiles(const P &p, int rows)
 template <bool F16, bool GATED, int XP, int NST, class P>
 void launch_few(const P &p, hipStream_t st)
 {
-    const int tn = (p.N + 15) / 16, tt = row_tiles(p, 8 * XP);
-    const dim3 grid(P::grouped ? tn * tt : tn, P::grouped ? 1 : tt);
-    k_linear_few<F16, GATED, XP, NST><<<grid, kFewWaves * 64, 0, st>>>(p, tn);
+    const dim3 grid((p.N + 15) / 16, (p.M + 8 * XP - 1) / (8 * XP));
+    k_linear_few<F16, GATED, XP, NST><<<grid, kFewWaves * 64, 0, st>>>(p);
 }
 
 template <bool F16, bool GATED, bool ANY, int TN, int TM, int WN, int WT, int NST, class P>
@@ -1490,25 +1717,41 @@ template <bool F16, bool GATED, class P>
 void launch_big(const P &p, int ksplit, hipStream_t st)
 {
     constexpr int NB = GATED ? 128 : 256;
-    const int tt = row_tiles(p, 256), tn = (p.N + NB - 1) / NB;
+    const int tt = (p.M + 255) / 256, tn = (p.N + NB - 1) / NB;
     if constexpr (P::mx) k_mx_big<F16, GATED><<<tn * tt * ksplit, 256, 0, st>>>(p, tn, tt, ksplit);
     else k_linear_big<F16, GATED><<<tn * tt * ksplit, 256, 0, st>>>(p, tn, tt, ksplit);
+    launch_join<F16, GATED>(p, ksplit, st);
+}
+
+template <bool F16, bool GATED, class P>
+void launch_pair(const P &p, int ksplit, hipStream_t st)
+{
+    constexpr int NB = GATED ? 128 : 256;
+    const int tt = row_tiles(p, 128), tn = (p.N + NB - 1) / NB;
+    k_linear_pair<F16, GATED><<<tn * tt * ksplit, 256, 0, st>>>(p, tn, tt, ksplit);
     if constexpr (!P::grouped) launch_join<F16, GATED>(p, ksplit, st);
 }
 
+// which kernels each kind of operands takes: linear.hip
 template <bool F16, bool GATED, class P>
 void launch_gated(const P &p, const LinearPlan &c, hipStream_t st)
 {
     switch (c.kind) {
-    case kFew1: return launch_few<F16, GATED, 1, GATED ? 2 : 3>(p, st);
-    case kFew2: return launch_few<F16, GATED, 2, 2>(p, st);
-    case kFew4: return launch_few<F16, GATED, 4, 2>(p, st);
     case kTile64x32: return launch_tile<F16, GATED, false, 64, 32, 2, 2, 6>(p, c.ksplit, st);
     case kTile64x64: return launch_tile<F16, GATED, false, 64, 64, 2, 2, P::mx ? 4 : 5>(p, c.ksplit, st);
     case kTile128x64: return launch_tile<F16, GATED, false, 128, 64, 4, 2, 6>(p, c.ksplit, st);
     case kTile128x128: return launch_tile<F16, GATED, false, 128, 128, 2, 4, 4>(p, c.ksplit, st);
-    case kBig: return launch_big<F16, GATED>(p, c.ksplit, st);
     }
+    if constexpr (!P::grouped) {
+        switch (c.kind) {
+        case kFew1: return launch_few<F16, GATED, 1, GATED ? 2 : 3>(p, st);
+        case kFew2: return launch_few<F16, GATED, 2, 2>(p, st);
+        case kFew4: return launch_few<F16, GATED, 4, 2>(p, st);
+        case kBig: return launch_big<F16, GATED>(p, c.ksplit, st);
+        }
+    }
+    if constexpr (P::mx || P::grouped)
+        if (c.kind == kTile256x128) return launch_pair<F16, GATED>(p, c.ksplit, st);
     if constexpr (!P::mx) {
         switch (c.kind) {
         case kAny64x32: return launch_tile<F16, GATED, true, 64, 32, 2, 2, 3>(p, c.ksplit, st);
