@@ -28,13 +28,18 @@ __device__ __forceinline__ uint64_t same_lanes(int id, bool on)
     return m;
 }
 
+// choices per wave of n (whole steps of 64, so that few choices take few
+// waves), and the waves that have any
+__device__ __forceinline__ int wave_run(int n) { return ((n + kGroupWaves - 1) / kGroupWaves + 63) & ~63; }
+__device__ __forceinline__ int waves_of(int n) { return n > 0 ? (n + wave_run(n) - 1) / wave_run(n) : 0; }
+
 // counts[w][e] of the block's waves, over choices [a, b) of the block
-__device__ __forceinline__ void count_choices(const int32_t *ids, int64_t a, int64_t b, int E, int *counts)
+__device__ __forceinline__ void count_choices(const int32_t *ids, int a, int b, int E, int *counts)
 {
     const int lane = threadIdx.x & 63, wv = threadIdx.x >> 6;
-    const int64_t per = (b - a + kGroupWaves - 1) / kGroupWaves, a0 = a + wv * per, b0 = min(b, a0 + per);
+    const int per = wave_run(b - a), a0 = a + wv * per, b0 = min(b, a0 + per);
     int *mine = counts + wv * E;
-    for (int64_t i = a0; i < b0; i += 64) {
+    for (int i = a0; i < b0; i += 64) {
         const int id = i + lane < b0 ? ids[i + lane] : -1;
         const bool on = (uint32_t)id < (uint32_t)E;
         const uint64_t same = same_lanes(id, on);
@@ -44,30 +49,32 @@ __device__ __forceinline__ void count_choices(const int32_t *ids, int64_t a, int
 
 // Grid: blocks of `per` choices each.  One block does all; of several, a first
 // launch writes their counts to hist [blocks][E].
-__global__ __launch_bounds__(kGroupThreads) void k_group_count(const int32_t *ids, int64_t R, int64_t per, int E, int32_t *hist)
+__global__ __launch_bounds__(kGroupThreads) void k_group_count(const int32_t *ids, int R, int per, int E, int32_t *hist)
 {
     __shared__ int lds_i[kGroupWaves * kMaxExperts];
-    for (int i = threadIdx.x; i < kGroupWaves * E; i += kGroupThreads) lds_i[i] = 0;
+    const int a = (int)blockIdx.x * per, b = min(R, a + per);
+    const int waves = waves_of(b - a);
+    for (int i = threadIdx.x; i < waves * E; i += kGroupThreads) lds_i[i] = 0;
     __syncthreads();
-    const int64_t a = blockIdx.x * per;
-    count_choices(ids, a, min(R, a + per), E, lds_i);
+    count_choices(ids, a, b, E, lds_i);
     __syncthreads();
     for (int e = threadIdx.x; e < E; e += kGroupThreads) {
         int s = 0;
-        for (int w = 0; w < kGroupWaves; w++) s += lds_i[w * E + e];
+        for (int w = 0; w < waves; w++) s += lds_i[w * E + e];
         hist[blockIdx.x * E + e] = s;
     }
 }
 
-__global__ __launch_bounds__(kGroupThreads) void k_group_place(const int32_t *ids, int64_t R, int64_t per, int k, int E,
+__global__ __launch_bounds__(kGroupThreads) void k_group_place(const int32_t *ids, int R, int per, int k, int E,
                                                                const int32_t *hist, int32_t *offsets, int32_t *tokens,
                                                                int32_t *places)
 {
     __shared__ int lds_i[kGroupWaves * kMaxExperts], sums[kGroupWaves];
     const int lane = threadIdx.x & 63, wv = threadIdx.x >> 6;
-    for (int i = threadIdx.x; i < kGroupWaves * E; i += kGroupThreads) lds_i[i] = 0;
+    const int a = (int)blockIdx.x * per, b = min(R, a + per);
+    const int waves = waves_of(b - a);
+    for (int i = threadIdx.x; i < waves * E; i += kGroupThreads) lds_i[i] = 0;
     __syncthreads();
-    const int64_t a = blockIdx.x * per, b = min(R, a + per);
     count_choices(ids, a, b, E, lds_i);
     __syncthreads();
     // thread e: the choices of expert e in the blocks before this one, in all,
@@ -75,17 +82,22 @@ __global__ __launch_bounds__(kGroupThreads) void k_group_place(const int32_t *id
     const int e = threadIdx.x;
     int before = 0, total = 0;
     if (e < E) {
-        for (int w = 0; w < kGroupWaves; w++) {
+        for (int w = 0; w < waves; w++) {
             const int c = lds_i[w * E + e];
             lds_i[w * E + e] = total;
             total += c;
         }
         if (gridDim.x > 1) {
             total = 0;
-            for (int g = 0; g < (int)gridDim.x; g++) {
-                const int c = hist[g * E + e];
-                if (g < (int)blockIdx.x) before += c;
-                total += c;
+            for (int g0 = 0; g0 < (int)gridDim.x; g0 += 16) {  // (16 loads on the way at once)
+                int c[16];
+#pragma unroll
+                for (int i = 0; i < 16; i++) c[i] = hist[min(g0 + i, (int)gridDim.x - 1) * E + e];
+#pragma unroll
+                for (int i = 0; i < 16; i++) {
+                    if (g0 + i < (int)blockIdx.x) before += c[i];
+                    if (g0 + i < (int)gridDim.x) total += c[i];
+                }
             }
         }
     }
@@ -100,17 +112,17 @@ __global__ __launch_bounds__(kGroupThreads) void k_group_place(const int32_t *id
     int base = scan - total;
     for (int w = 0; w < wv; w++) base += sums[w];
     if (e < E) {
-        for (int w = 0; w < kGroupWaves; w++) lds_i[w * E + e] += base + before;
+        for (int w = 0; w < waves; w++) lds_i[w * E + e] += base + before;
         if (blockIdx.x == 0) {
             offsets[e] = base;
             if (e == E - 1) offsets[E] = base + total;
         }
     }
     __syncthreads();
-    const int64_t run = (b - a + kGroupWaves - 1) / kGroupWaves, a0 = a + wv * run, b0 = min(b, a0 + run);
+    const int run = wave_run(b - a), a0 = a + wv * run, b0 = min(b, a0 + run);
     int *mine = lds_i + wv * E;
-    for (int64_t i = a0; i < b0; i += 64) {
-        const int64_t c = i + lane;
+    for (int i = a0; i < b0; i += 64) {
+        const int c = i + lane;
         const int id = c < b0 ? ids[c] : -1;
         const bool on = (uint32_t)id < (uint32_t)E;
         const uint64_t same = same_lanes(id, on), lower = same & ((1ull << lane) - 1);
@@ -119,7 +131,7 @@ __global__ __launch_bounds__(kGroupThreads) void k_group_place(const int32_t *id
             const int first = mine[id];
             place = first + __popcll(lower);
             if (lower == 0) mine[id] = first + __popcll(same);
-            tokens[place] = (int32_t)(c / k);
+            tokens[place] = (int)((uint32_t)c / (uint32_t)k);
         }
         if (c < b0) places[c] = place;
     }
@@ -127,35 +139,54 @@ __global__ __launch_bounds__(kGroupThreads) void k_group_place(const int32_t *id
 
 // --------------------------------------------------------------- combination
 
-// eight values of a row in fp32
-__device__ __forceinline__ void read8(const void *p, int type, int64_t at, int n, float (&v)[8])
+// eight values of a row as they are in memory (n of them), and in fp32
+struct Raw8 {
+    uint4 q[2];
+};
+__device__ __forceinline__ Raw8 load8_raw(const void *p, int type, int64_t at, int n)
 {
+    Raw8 r = {{make_uint4(0, 0, 0, 0), make_uint4(0, 0, 0, 0)}};
     if (type == MOE_F32) {
         const float *f = reinterpret_cast<const float *>(p) + at;
         if (n >= 8) {
-            __builtin_memcpy(v, f, 32);
+            __builtin_memcpy(&r, f, 32);
         } else {
+            float v[8] = {};
 #pragma unroll
-            for (int j = 0; j < 8; j++) v[j] = j < n ? f[j] : 0.0f;
+            for (int j = 0; j < 8; j++)
+                if (j < n) v[j] = f[j];
+            __builtin_memcpy(&r, v, 32);
         }
-        return;
+        return r;
     }
     const uint16_t *h = reinterpret_cast<const uint16_t *>(p) + at;
-    uint16_t q[8] = {0, 0, 0, 0, 0, 0, 0, 0};
     if (n >= 8) {
-        __builtin_memcpy(q, h, 16);
+        __builtin_memcpy(&r, h, 16);
     } else {
+        uint16_t v[8] = {};
 #pragma unroll
         for (int j = 0; j < 8; j++)
-            if (j < n) q[j] = h[j];
+            if (j < n) v[j] = h[j];
+        __builtin_memcpy(&r, v, 16);
     }
+    return r;
+}
+__device__ __forceinline__ void to_f32(const Raw8 &r, int type, float (&v)[8])
+{
+    if (type == MOE_F32) {
+        __builtin_memcpy(v, &r, 32);
+        return;
+    }
+    uint16_t q[8];
+    __builtin_memcpy(q, &r, 16);
 #pragma unroll
     for (int j = 0; j < 8; j++)
         v[j] = type == MOE_F16 ? (float)__builtin_bit_cast(_Float16, q[j]) : __uint_as_float((uint32_t)q[j] << 16);
 }
 
 // A thread adds eight columns of a token's rows, in the order of its choices,
-// fp32 throughout; YT: the rows' type.
+// fp32 throughout; YT: the rows' type.  Eight rows are on the way at once; a
+// choice without a row reads one that is there and adds nothing.
 template <int YT>
 __global__ __launch_bounds__(256) void k_group_combine(CombineParams p)
 {
@@ -165,29 +196,36 @@ __global__ __launch_bounds__(256) void k_group_combine(CombineParams p)
     const int32_t *pl = p.places + (int64_t)t * p.k;
     const float *wt = p.weights ? p.weights + (int64_t)t * p.k : nullptr;
     float s[8] = {};
-    constexpr int B = 4;
-    for (int j0 = 0; j0 < p.k; j0 += B) {
-        float v[B][8], w[B];
+    Raw8 res = {};
+    if (p.res) res = load8_raw(p.res, p.res_type, (int64_t)t * p.ldr + n0, n);
+    constexpr int B = 8;
+    for (int j0 = 0; j0 < (p.rows > 0 ? p.k : 0); j0 += B) {
+        Raw8 v[B];
+        float w[B];
+        bool on[B];
+        int64_t at[B];
 #pragma unroll
         for (int j = 0; j < B; j++) {
             const int place = j0 + j < p.k ? pl[j0 + j] : -1;
-            const bool on = (uint32_t)place < (uint32_t)p.rows;
-            w[j] = on ? (wt ? wt[j0 + j] : 1.0f) : 0.0f;
-            if (on) {
-                read8(p.y, YT, (int64_t)place * p.ldy + n0, n, v[j]);
-            } else {
-#pragma unroll
-                for (int i = 0; i < 8; i++) v[j][i] = 0.0f;
-            }
+            on[j] = (uint32_t)place < (uint32_t)p.rows;
+            w[j] = on[j] ? (wt ? wt[j0 + j] : 1.0f) : 0.0f;
+            at[j] = (int64_t)(on[j] ? place : 0) * p.ldy + n0;
         }
 #pragma unroll
         for (int j = 0; j < B; j++)
+            if (j0 + j < p.k) v[j] = load8_raw(p.y, YT, at[j], n);
 #pragma unroll
-            for (int i = 0; i < 8; i++) s[i] = fmaf(w[j], v[j][i], s[i]);
+        for (int j = 0; j < B; j++) {
+            if (!on[j]) continue;
+            float f[8];
+            to_f32(v[j], YT, f);
+#pragma unroll
+            for (int i = 0; i < 8; i++) s[i] = fmaf(w[j], f[i], s[i]);
+        }
     }
     if (p.res) {
         float r[8];
-        read8(p.res, p.res_type, (int64_t)t * p.ldr + n0, n, r);
+        to_f32(res, p.res_type, r);
 #pragma unroll
         for (int i = 0; i < 8; i++) s[i] += r[i];
     }
@@ -217,20 +255,20 @@ __global__ __launch_bounds__(256) void k_group_combine(CombineParams p)
 }
 
 // choices of a block and the blocks of a call
-int64_t group_per(int64_t R) { return std::max<int64_t>(4096, (R + 63) / 64); }
+int64_t group_per(int64_t R) { return std::max<int64_t>(1024, (R + 63) / 64); }
 
 }  // namespace
 
 size_t group_workspace(int64_t R, int E) { return R > group_per(R) ? (size_t)((R + group_per(R) - 1) / group_per(R)) * E * 4 : 256; }
 
+// (R: 2^26 at most)
 hipError_t launch_group(const int32_t *ids, int64_t R, int k, int E, int32_t *offsets, int32_t *tokens, int32_t *places,
                         void *ws, hipStream_t st)
 {
-    const int64_t per = group_per(R);
-    const int blocks = (int)std::max<int64_t>(1, (R + per - 1) / per);
+    const int per = (int)group_per(R), blocks = (int)std::max<int64_t>(1, (R + per - 1) / per);
     int32_t *hist = reinterpret_cast<int32_t *>(ws);
-    if (blocks > 1) k_group_count<<<blocks, kGroupThreads, 0, st>>>(ids, R, per, E, hist);
-    k_group_place<<<blocks, kGroupThreads, 0, st>>>(ids, R, per, k, E, hist, offsets, tokens, places);
+    if (blocks > 1) k_group_count<<<blocks, kGroupThreads, 0, st>>>(ids, (int)R, per, E, hist);
+    k_group_place<<<blocks, kGroupThreads, 0, st>>>(ids, (int)R, per, k, E, hist, offsets, tokens, places);
     return hipGetLastError();
 }
 

@@ -177,8 +177,8 @@ struct GroupedKind {
 constexpr GroupedKind kGroupedKinds[] = {
     {kTile64x32, 64, 32, 130, 2350, false},    {kTile64x64, 64, 64, 180, 2750, false},
     {kTile128x64, 128, 64, 310, 4500, false},  {kTile128x128, 128, 128, 500, 6000, false},
-    {kTile256x128, 256, 128, 950, 5000, false}, {kAny64x32, 64, 32, 400, 2500, true},
-    {kAny64x64, 64, 64, 500, 3000, true},      {kAny128x128, 128, 128, 950, 6500, true},
+    {kTile256x128, 256, 128, 950, 5000, false}, {kAny64x32, 64, 32, 290, 1900, true},
+    {kAny64x64, 64, 64, 400, 3000, true},      {kAny128x128, 128, 128, 950, 6500, true},
 };
 
 }  // namespace

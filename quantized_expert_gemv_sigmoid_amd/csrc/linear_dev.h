@@ -354,23 +354,30 @@ __device__ __forceinline__ bool block_tile(P &p, int tn, int tt, int &t0, int &n
             const int v = __shfl_up(upto, d, 64);
             if (lane >= d) upto += v;
         }
-        const int tiles = __builtin_amdgcn_readlane(upto, 63);
-        const int per8 = tn * tiles, x = blockIdx.x & 7;
-        if ((int)(blockIdx.x >> 3) >= (per8 >> 3) + (x < (per8 & 7) ? 1 : 0)) return false;
-        int ti;
-        tile_of(blockIdx.x, tn, tiles, ni, ti);
+        // the blocks of one XCD (block % 8) take a run of tiles; a group's, up to
+        // eight of its row tiles by all weight tiles, so that the blocks that
+        // its CUs hold read a weight tile into its L2 once
+        const int total = tn * __builtin_amdgcn_readlane(upto, 63), x = blockIdx.x & 7, at = blockIdx.x >> 3;
+        if (at >= (total >> 3) + (x < (total & 7) ? 1 : 0)) return false;
+        const int l = x * (total >> 3) + min(x, total & 7) + at, ti = l / tn;
         const uint64_t past = __ballot(upto > ti);
         if (!past) return false;
         const int owner = __builtin_ctzll(past);
-        int left = ti - (upto - mine), g = 0, first = 0, end = 0;
+        int left = ti - (upto - mine), g = 0, first = 0, end = 0, before = upto - mine, own = 0;
         for (int i = 0, a = start(g0); i < per; i++) {
             const int b = start(g0 + i + 1), n = (max(b - a, 0) + TM - 1) / TM;
-            if (left >= 0 && left < n) g = g0 + i, first = a + left * TM, end = b;
+            if (left >= 0 && left < n) g = g0 + i, first = a, end = b, own = n;
+            if (left >= n) before += n;
             left -= n;
             a = b;
         }
         g = __builtin_amdgcn_readlane(g, owner);
-        t0 = __builtin_amdgcn_readlane(first, owner);
+        first = __builtin_amdgcn_readlane(first, owner);
+        own = __builtin_amdgcn_readlane(own, owner);
+        const int r = l - __builtin_amdgcn_readlane(before, owner) * tn, q = r / (8 * tn), in = r - q * 8 * tn;
+        const int h = min(8, own - 8 * q);
+        ni = in / h;
+        t0 = first + (8 * q + in % h) * TM;
         p.M = __builtin_amdgcn_readlane(end, owner);
         p.w = reinterpret_cast<const uint16_t *>(p.w) + g * p.wstride;
         if (p.w_up) p.w_up = reinterpret_cast<const uint16_t *>(p.w_up) + g * p.wstride;
@@ -1457,10 +1464,8 @@ __global__ __launch_bounds__(256, 2) void k_linear_pair(P p, int tn, int tt, int
                 if constexpr (P::mx)
                     acc[q][f][g] = mfma_mx(a[q & 1][st][f], sa[q & 1][st][f], b[st][g], sb[st][g], acc[q][f][g]);
                 else acc[q][f][g] = mfma16v(a[q & 1][st][f], b[st][g], acc[q][f][g]);
-                __builtin_amdgcn_sched_barrier(0);
                 if (i % 4 == 1 && i / 4 < G::C)
                     copy(i / 4, (q + 1) & 3, q == 3 ? s + 2 : s + 1, slot, true, q == 0 ? s + 1 : s + 2);
-                __builtin_amdgcn_sched_barrier(0);
             }
             slot = next;
         }

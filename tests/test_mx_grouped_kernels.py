@@ -38,7 +38,7 @@ MX = [
 GROUPED = [
     (0, 3, 0, 2, 4, 40, 9), (0, 3, 1, 2, 4, 40, 9), (0, 4, 0, 9, 518, 64, 11), (0, 4, 1, 5, 482, 48, 9),
     (0, 5, 0, 173, 1461, 56, 75), (0, 5, 1, 261, 636, 64, 37), (0, 6, 0, 13, 2581, 48, 81), (0, 6, 1, 4, 4417, 40, 40),
-    (0, 7, 0, 2, 6, 103, 18), (0, 7, 1, 2, 6, 68, 15), (0, 8, 0, 20, 1378, 45, 22), (0, 8, 1, 2, 786, 55, 35),
+    (0, 7, 0, 2, 6, 103, 18), (0, 7, 1, 2, 6, 68, 15), (0, 8, 0, 4, 4008, 55, 9), (0, 8, 1, 34, 6608, 45, 10),
     (0, 9, 0, 24, 4046, 54, 80), (0, 9, 1, 7, 3335, 41, 51), (0, 11, 0, 23, 48, 40, 642), (0, 11, 1, 37, 74, 56, 230),
     (1, 3, 0, 2, 6, 256, 9), (1, 3, 1, 2, 4, 256, 25), (1, 4, 0, 3, 452, 256, 10), (1, 4, 1, 3, 498, 256, 15),
     (1, 5, 0, 276, 786, 256, 65), (1, 5, 1, 265, 615, 384, 44), (1, 6, 0, 2, 3189, 256, 70),
