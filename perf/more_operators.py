@@ -227,7 +227,7 @@ def prepare(case, seed):
         s["tokens"] = torch.empty(R, dtype=torch.int32, device="cuda")
         s["places"] = torch.empty(T, k, dtype=torch.int32, device="cuda")
         s["h"] = torch.empty(R, F, dtype=t, device="cuda")
-        s["y"] = torch.empty(R, K, dtype=t, device="cuda")
+        s["y"] = torch.empty(R, K, device="cuda")  # 32 bits until the rows of a token are added up
         s["out"] = torch.empty(T, K, dtype=t, device="cuda")
     return s
 
@@ -284,7 +284,7 @@ def _own(s, case):
         return s["out"]
     moe.group(s["ids"], T, case["E"], s["offsets"], s["tokens"], s["places"], s["ws"])
     moe.grouped_linear(s["up_desc"], s["x"], s["offsets"], R, s["h"], None, moe.OUT_HALF, rows=s["tokens"])
-    moe.grouped_linear(s["down_desc"], s["h"], s["offsets"], R, s["y"], None, moe.OUT_HALF)
+    moe.grouped_linear(s["down_desc"], s["h"], s["offsets"], R, None, s["y"], moe.OUT_F32)
     moe.combine(s["y"], R, s["places"], s["weights"], T, s["out"], residual=s["residual"])
     return {"out": s["out"], "offsets": s["offsets"], "places": s["places"]}
 
