@@ -404,16 +404,18 @@ def make_latent_desc(n_experts: int, top_k: int, hidden: int, latent: int, d_ffn
 
 _torch = None  # torch, and what a call looks up in it
 _types = {}    # dtype -> moe_type
-_raw_stream = None
+_raw_stream = _current = None
 
 
 def _setup() -> None:
-    global _torch, _raw_stream
+    global _torch, _raw_stream, _current
     import torch
     _types.update({torch.bfloat16: BF16, torch.float16: F16, torch.float32: F32})
     # (the current stream's address without a Stream object around it, where torch has it)
     _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
         lambda i: torch.cuda.current_stream(i).cuda_stream)
+    # (and the current device's number, where torch has it by itself: of a tensor there, so CUDA is initialised)
+    _current = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
     _torch = torch
 
 
@@ -429,7 +431,10 @@ def _type_of(t) -> int:
 
 def _rows(t, rows: int, cols: int, what: str) -> int:
     """Elements between the rows of a tensor of at least `rows` rows of `cols` contiguous values (one row has none: cols)."""
-    shape, stride = t.shape, t.stride()
+    shape = t.shape
+    if len(shape) == 2 and shape[0] >= rows and shape[1] == cols and t.is_contiguous():
+        return cols
+    stride = t.stride()
     if len(shape) != 2 or shape[0] < rows or shape[1] != cols or (stride[1] != 1 and cols > 1):
         raise MoeError(EINVAL, f"{what}: {rows} rows of {cols} contiguous values wanted, got {tuple(shape)}, strides {tuple(stride)}")
     return stride[0] if rows > 1 else cols
@@ -446,9 +451,17 @@ def _flat(t, n: int, dtype, what: str):
 
 def _same_device(desc, first, *others) -> None:
     """The tensors of a call lie on one device, and those of the descriptor (desc.device, where known) too."""
+    i = first.get_device()
+    known = None if desc is None else desc.device
+    if i >= 0 and (known is None or known.index == i):
+        for t in others:
+            if t is not None and t.get_device() != i:
+                break
+        else:
+            return
     d = first.device
-    if desc is not None and desc.device is not None and desc.device != d:
-        raise MoeError(EINVAL, f"tensors on {desc.device} and {d}")
+    if known is not None and known != d:
+        raise MoeError(EINVAL, f"tensors on {known} and {d}")
     for t in others:
         if t is not None and t.device != d:
             raise MoeError(EINVAL, f"tensors on {d} and {t.device}")
@@ -460,11 +473,11 @@ def _ws_tensor(ws) -> tuple:
 
 def _call(x, stream, f, *args) -> int:
     """f(*args, stream) on x's device: that device's current stream where none is given."""
-    i = x.device.index
-    if i is None:  # (not a GPU's: the arguments that were refused first aside, there is nothing to launch on)
+    i = x.get_device()
+    if i < 0:  # (not a GPU's: the arguments that were refused first aside, there is nothing to launch on)
         raise MoeError(EINVAL, f"tensors on {x.device}")
     s = _raw_stream(i) if stream is None else _stream(stream)
-    if i != _torch.cuda.current_device():
+    if i != _current():
         with _torch.cuda.device(i):
             return f(*args, s)
     return f(*args, s)

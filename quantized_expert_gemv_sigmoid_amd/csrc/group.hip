@@ -1,6 +1,7 @@
 // The choices of tokens sorted by expert (moe_group), and the experts' rows
 // added up again (moe_combine).
 #include <algorithm>
+#include <type_traits>
 
 #include "../../include/moe.h"
 #include "common.h"
@@ -185,9 +186,9 @@ __device__ __forceinline__ void to_f32(const Raw8 &r, int type, float (&v)[8])
 }
 
 // A thread adds eight columns of a token's rows, in the order of its choices,
-// fp32 throughout; YT: the rows' type.  Eight rows are on the way at once; a
-// choice without a row reads one that is there and adds nothing.
-template <int YT>
+// fp32 throughout; YT: the rows' type.  B rows are on the way at once; a choice
+// without a row reads one that is there and adds nothing.
+template <int YT, int B>
 __global__ __launch_bounds__(256) void k_group_combine(CombineParams p)
 {
     const int t = blockIdx.y + p.t0, n0 = (blockIdx.x * 256 + threadIdx.x) * 8;
@@ -198,7 +199,6 @@ __global__ __launch_bounds__(256) void k_group_combine(CombineParams p)
     float s[8] = {};
     Raw8 res = {};
     if (p.res) res = load8_raw(p.res, p.res_type, (int64_t)t * p.ldr + n0, n);
-    constexpr int B = 8;
     for (int j0 = 0; j0 < (p.rows > 0 ? p.k : 0); j0 += B) {
         Raw8 v[B];
         float w[B];
@@ -278,9 +278,14 @@ hipError_t launch_group_combine(const CombineParams &params, int y_type, hipStre
     const int total = p.T;
     for (p.t0 = 0; p.t0 < total; p.t0 += 65535) {
         const dim3 grid((p.n + 2047) / 2048, std::min(65535, total - p.t0));
-        if (y_type == MOE_F32) k_group_combine<MOE_F32><<<grid, 256, 0, st>>>(p);
-        else if (y_type == MOE_F16) k_group_combine<MOE_F16><<<grid, 256, 0, st>>>(p);
-        else k_group_combine<MOE_BF16><<<grid, 256, 0, st>>>(p);
+        auto go = [&](auto type) {
+            constexpr int YT = decltype(type)::value;
+            if (p.k <= 8) k_group_combine<YT, 8><<<grid, 256, 0, st>>>(p);
+            else k_group_combine<YT, 16><<<grid, 256, 0, st>>>(p);
+        };
+        if (y_type == MOE_F32) go(std::integral_constant<int, MOE_F32>{});
+        else if (y_type == MOE_F16) go(std::integral_constant<int, MOE_F16>{});
+        else go(std::integral_constant<int, MOE_BF16>{});
     }
     return hipGetLastError();
 }

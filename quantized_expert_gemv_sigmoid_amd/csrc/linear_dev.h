@@ -341,13 +341,20 @@ __device__ __forceinline__ bool block_tile(P &p, int tn, int tt, int &t0, int &n
         return true;
     } else {
         const int lane = threadIdx.x & 63, per = (p.groups + 63) >> 6, g0 = lane * per;
-        auto start = [&](int g) { return min(max(p.offsets[min(g, p.groups)], 0), p.M); };
+        constexpr int PER = kMaxExperts / 64;
+        int o[PER + 1];  // (all loads on the way at once)
+        auto load = [&](auto n) {
+#pragma unroll
+            for (int i = 0; i <= decltype(n)::value; i++) o[i] = p.offsets[min(g0 + i, p.groups)];
+#pragma unroll
+            for (int i = 0; i <= PER; i++) o[i] = i <= min(per, decltype(n)::value) ? min(max(o[i], 0), p.M) : 0;
+        };
+        if (per <= 2) load(std::integral_constant<int, 2>{});
+        else load(std::integral_constant<int, PER>{});
+        auto tiles_of = [&](int i) { return i < per ? (max(o[i + 1] - o[i], 0) + TM - 1) / TM : 0; };
         int mine = 0;
-        for (int i = 0, a = start(g0); i < per; i++) {
-            const int b = start(g0 + i + 1);
-            mine += (max(b - a, 0) + TM - 1) / TM;
-            a = b;
-        }
+#pragma unroll
+        for (int i = 0; i < PER; i++) mine += tiles_of(i);
         int upto = mine;
 #pragma unroll
         for (int d = 1; d < 64; d <<= 1) {
@@ -364,12 +371,12 @@ __device__ __forceinline__ bool block_tile(P &p, int tn, int tt, int &t0, int &n
         if (!past) return false;
         const int owner = __builtin_ctzll(past);
         int left = ti - (upto - mine), g = 0, first = 0, end = 0, before = upto - mine, own = 0;
-        for (int i = 0, a = start(g0); i < per; i++) {
-            const int b = start(g0 + i + 1), n = (max(b - a, 0) + TM - 1) / TM;
-            if (left >= 0 && left < n) g = g0 + i, first = a, end = b, own = n;
+#pragma unroll
+        for (int i = 0; i < PER; i++) {
+            const int n = tiles_of(i);
+            if (left >= 0 && left < n) g = g0 + i, first = o[i], end = o[i + 1], own = n;
             if (left >= n) before += n;
             left -= n;
-            a = b;
         }
         g = __builtin_amdgcn_readlane(g, owner);
         first = __builtin_amdgcn_readlane(first, owner);
