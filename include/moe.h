@@ -555,8 +555,9 @@ int32_t moe_grouped_path_for(const moe_grouped_desc *desc, const void *x, int64_
  * behind each row, a row of zeros for one outside [0, x_rows); or NULL: row r
  * is x's own (x_rows >= R).  offsets: [n_groups + 1], not decreasing; rows
  * before offsets[0] and from min(offsets[n_groups], R) on are left as they
- * are.  Offsets outside [0, R] count as its ends.  rows and offsets are read on
- * the device, so the call needs no synchronisation behind moe_group.
+ * are.  Offsets outside [0, R] count as its ends (where they decrease, which
+ * rows are written is not defined; none outside [0, R) is).  rows and offsets
+ * are read on the device, so the call needs no synchronisation behind moe_group.
  *
  * 0 <= R <= 2^24; ldx, ldw, ldo up to 2^22 (MXFP4: ldx, ldw up to 2^23, ldxs,
  * ldw_s to 2^22); with `rows`, x's rows lie within 2 GiB.  MXFP4: n_in a multiple
@@ -577,7 +578,8 @@ moe_status moe_grouped_linear(const moe_grouped_desc *desc, const void *x, int64
  * residual: NULL, or T rows ldr apart (0: the same row for every token).
  * y, residual and out (rows ldo apart) each have a moe_type of their own
  * (MOE_BF16, MOE_F16, MOE_F32).  out may be the residual's own buffer (same
- * pointer, row distance and type).  k up to 64, n up to 2^20.
+ * pointer, row distance and type); otherwise it must not overlap inputs.  k up
+ * to 64, n up to 2^20.
  */
 moe_status moe_combine(const void *y, int32_t y_type, int64_t ldy, int32_t R, const int32_t *places, const float *weights, int32_t T,
                        int32_t top_k, int32_t n, const void *residual, int32_t residual_type, int64_t ldr, void *out,

@@ -276,6 +276,13 @@ __device__ __forceinline__ void barrier()
 typedef uint32_t u32x2_t __attribute__((ext_vector_type(2)));
 typedef uint16_t u16x2_t __attribute__((ext_vector_type(2)));
 
+// MXFP4: a lane's two products of a stage take neighbouring blocks, pieces 2 q
+// and 2 q + 1 of its row (16-bit rows: q and 4 + q), so that both scales come
+// in one read; their places in LDS are permuted by this of row / 2, for which
+// the lanes that LDS serves together (0-3, 12-15, 20-27 and so on) touch every
+// bank alike.
+__device__ __forceinline__ int mx_place(int i) { return (i & 1) | ((i & 4) >> 1) | (((i >> 1) ^ (i >> 2)) & 1) << 2; }
+
 template <bool F16>
 struct Frag {
     using V = typename std::conditional<F16, f16x8_t, bf16x8_t>::type;
@@ -382,10 +389,11 @@ __device__ __forceinline__ bool block_tile(P &p, int tn, int tt, int &t0, int &n
         first = __builtin_amdgcn_readlane(first, owner);
         own = __builtin_amdgcn_readlane(own, owner);
         const int r = l - __builtin_amdgcn_readlane(before, owner) * tn, q = r / (8 * tn), in = r - q * 8 * tn;
-        const int h = min(8, own - 8 * q);
+        const int h = max(1, min(8, own - 8 * q));
         ni = in / h;
         t0 = first + (8 * q + in % h) * TM;
         p.M = __builtin_amdgcn_readlane(end, owner);
+        if (t0 >= p.M || ni >= tn) return false;  // (only where offsets decrease)
         p.w = reinterpret_cast<const uint16_t *>(p.w) + g * p.wstride;
         if (p.w_up) p.w_up = reinterpret_cast<const uint16_t *>(p.w_up) + g * p.wstride;
         const int64_t bias = g * p.bstride * (p.bias_f32 ? 4 : 2);
@@ -397,12 +405,6 @@ __device__ __forceinline__ bool block_tile(P &p, int tn, int tt, int &t0, int &n
         }
         return true;
     }
-}
-
-template <class P>
-__device__ __forceinline__ int group_start(const P &p, int g)
-{
-    return min(max(p.offsets[min(g, p.groups)], 0), p.M);
 }
 
 template <class P>
@@ -755,12 +757,19 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(1, 1))) voi
 
 // ------------------------------------------- whole prompts: 256 x 256, MXFP4
 
-// c += a b, 16 x 16 x 128 codes and a scale for each lane's 32, c in accumulation registers
+// c += a b, 16 x 16 x 128 codes and a scale for each lane's 32 (byte B of sa
+// and sb), c in accumulation registers
+template <int B>
 __device__ __forceinline__ void mfma16_mx(u32x4_t a, int sa, u32x4_t b, int sb, f32x4_t &c)
 {
-    asm volatile("v_mfma_scale_f32_16x16x128_f8f6f4 %0, %1, %2, %0, %3, %4 op_sel_hi:[0,0,0] cbsz:4 blgp:4"
-                 : "+a"(c)
-                 : "v"(a), "v"(b), "v"(sa), "v"(sb));
+    if (B == 0)
+        asm volatile("v_mfma_scale_f32_16x16x128_f8f6f4 %0, %1, %2, %0, %3, %4 op_sel_hi:[0,0,0] cbsz:4 blgp:4"
+                     : "+a"(c)
+                     : "v"(a), "v"(b), "v"(sa), "v"(sb));
+    else
+        asm volatile("v_mfma_scale_f32_16x16x128_f8f6f4 %0, %1, %2, %0, %3, %4 op_sel:[1,1,0] op_sel_hi:[0,0,0] cbsz:4 blgp:4"
+                     : "+a"(c)
+                     : "v"(a), "v"(b), "v"(sa), "v"(sb));
 }
 
 constexpr int kMxUnit = kUnit + 128 * 8;  // 128 rows x 256 codes and their scales
@@ -800,17 +809,17 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(1, 1))) voi
 
     // copies: the wave's 32 rows of a unit in four pieces of 8, this lane's 16
     // bytes of each, and half a row's scales
-    const int l8 = lane >> 3, piece = (lane & 7) ^ (l8 >> 1);
+    const int l8 = lane >> 3, piece = (lane & 7) ^ mx_place(l8 >> 1);
     uint32_t va[4], vb[4];
 #pragma unroll
     for (int j = 0; j < 4; j++) {
-        const uint32_t row = 32 * wv + 8 * j + l8, col = (piece ^ (j & 1 ? 4 : 0)) * 16;
+        const uint32_t row = 32 * wv + 8 * j + l8, col = (piece ^ (j & 1 ? 6 : 0)) * 16;
         va[j] = (uint32_t)(row * p.ldw * 2) + col;
         vb[j] = (uint32_t)(row * p.ldx * 2) + col;
     }
     const int srow = 32 * wv + (lane >> 1), sh = (lane & 1) * 4;
     uint32_t vas = (uint32_t)(srow * p.ldws) + sh, vbs = (uint32_t)(srow * p.ldxs) + sh;
-    int kc0 = piece * 8, kc1 = (piece ^ 4) * 8, kcs = sh * 8;
+    int kc0 = piece * 8, kc1 = (piece ^ 6) * 8, kcs = sh * 8;
     const uint32_t m0w = (uint32_t)(uintptr_t)lds + wv * 4096, m0s = (uint32_t)(uintptr_t)lds + kUnit + wv * 256;
     constexpr int A0 = 0, A1 = kMxUnit, B0 = 2 * kMxUnit, B1 = 3 * kMxUnit, BUF = 4 * kMxUnit;
     // piece j of the wave's part of a unit, its scales as piece 4, D stages on
@@ -833,19 +842,19 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(1, 1))) voi
     const LDS uint8_t *fa[3], *fb[3];  // in the buffer that is read next: fragments of both steps, scales
 #pragma unroll
     for (int st = 0; st < 2; st++) {
-        const int o = r16 * 128 + (((st * 4 + q4) ^ (r16 >> 1)) << 4);
+        const int o = r16 * 128 + (((2 * q4 + st) ^ mx_place(r16 >> 1)) << 4);
         fa[st] = lds + wn * 64 * 128 + o;
         fb[st] = lds + wt * 64 * 128 + o;
     }
-    fa[2] = lds + kUnit + (wn * 64 + r16) * 8 + q4;
-    fb[2] = lds + kUnit + (wt * 64 + r16) * 8 + q4;
+    fa[2] = lds + kUnit + (wn * 64 + r16) * 8 + 2 * q4;
+    fb[2] = lds + kUnit + (wt * 64 + r16) * 8 + 2 * q4;
     struct Half {  // 64 rows x 256 codes: [step][16 rows]
         u32x4_t f[2][4];
-        int s[2][4];
+        int s[4];  // both steps' scales
     };
     Half a0, a1, b0, b1;
     auto fetch = [&](Half &h, const LDS uint8_t *const(&q)[3], int at, int i) {
-        h.s[i >> 2][i & 3] = q[2][at + (i & 3) * 128 + (i >> 2) * 4];
+        if (i < 4) h.s[i] = *reinterpret_cast<const LDS uint16_t *>(q[2] + at + i * 128);
         h.f[i >> 2][i & 3] = __builtin_bit_cast(u32x4_t, lds_ld16(q[i >> 2] + at + (i & 3) * 2048));
     };
     auto readA = [&](Half &a, int at, int i) { fetch(a, fa, at, i); };
@@ -880,17 +889,18 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(1, 1))) voi
     }
     wait_copies<30>();  // (these reads too: the first two phases fill the units anew)
 
-    // the phases of k_linear_big; a read is one of a fragment and one of its scales
+    // the phases of k_linear_big, with the scales of a half read beside its first fragments
     auto phase = [&](auto check, auto d, __amdgpu_buffer_rsrc_t r, __amdgpu_buffer_rsrc_t s, int at, bool b, f32x4_t(&c)[4][4],
                      const Half &x, const Half &y, auto read) {
         __builtin_amdgcn_sched_barrier(0);
-        wait_copies<25, 14>();
+        wait_copies<25, 12>();
         barrier();
         __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
         for (int i = 0; i < 32; i++) {
             const int st = i >> 4, f = (i >> 2) & 3, g = f & 1 ? 3 - (i & 3) : i & 3;
-            mfma16_mx(x.f[st][f], x.s[st][f], y.f[st][g], y.s[st][g], c[f][g]);
+            if (st == 0) mfma16_mx<0>(x.f[st][f], x.s[f], y.f[st][g], y.s[g], c[f][g]);
+            else mfma16_mx<1>(x.f[st][f], x.s[f], y.f[st][g], y.s[g], c[f][g]);
             if (i % 4 == 0) read(i >> 2);
             if (i % 6 == 2 && i < 30) copy(check, d, r, s, at, b, i / 6);
             __builtin_amdgcn_sched_barrier(0);
@@ -950,15 +960,15 @@ __device__ __forceinline__ f32x4_t mfma16v(f16x8_t a, f16x8_t b, f32x4_t c)
     return __builtin_amdgcn_mfma_f32_16x16x32_f16(a, b, c, 0, 0, 0);
 }
 
-// 128 codes a row, one scale for a lane's 32
-template <class V>
+// 128 codes a row, one scale for a lane's 32: byte B of sa and sb
+template <int B, class V>
 __device__ __forceinline__ f32x4_t mfma_mx(V a, int sa, V b, int sb, f32x4_t c)
 {
     typedef int i32x8_t __attribute__((ext_vector_type(8)));
     const uint4 x = __builtin_bit_cast(uint4, a), y = __builtin_bit_cast(uint4, b);
     const i32x8_t xa = {(int)x.x, (int)x.y, (int)x.z, (int)x.w, 0, 0, 0, 0};
     const i32x8_t yb = {(int)y.x, (int)y.y, (int)y.z, (int)y.w, 0, 0, 0, 0};
-    return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(xa, yb, c, 4, 4, 0, sa, 0, sb);
+    return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(xa, yb, c, 4, 4, B, sa, B, sb);
 }
 
 // TN weight rows (gated: TN / 2 of each matrix) x TM tokens per block, K in a
@@ -1023,7 +1033,7 @@ __global__ __launch_bounds__(WN * WT * 64) void k_linear_tile(P p, int tn, int t
     const int l8 = lane >> 3;
     const uint32_t lbase = (uint32_t)(uintptr_t)lds + wv * 1024;
     uint32_t cv[G::CW];
-    const int kc = ((lane & 7) ^ ((4 * wv + (l8 >> 1)) & 7)) * 8;  // this lane's k in them
+    const int rot = (4 * wv + (l8 >> 1)) & 7, kc = ((lane & 7) ^ (P::mx ? mx_place(rot) : rot)) * 8;  // this lane's k in them
 #pragma unroll
     for (int j = 0; j < G::CW; j++) {
         const int pc = wv + G::NW * j;
@@ -1100,22 +1110,23 @@ __global__ __launch_bounds__(WN * WT * 64) void k_linear_tile(P p, int tn, int t
     int fa[2], fb[2];
 #pragma unroll
     for (int st = 0; st < 2; st++) {
-        const int o = r16 * 128 + (((st * 4 + q4) ^ (r16 >> 1)) << 4);
+        const int o = r16 * 128 + ((P::mx ? (2 * q4 + st) ^ mx_place(r16 >> 1) : (st * 4 + q4) ^ (r16 >> 1)) << 4);
         fa[st] = wn * (TN / 2 / WN) * 128 + o;
         fb[st] = TN * 128 + wt * (TM / WT) * 128 + o;
     }
     constexpr int FA = 2 * G::FN, FT = G::FT, NM = FA * FT, NR = FA + FT;
     f32x4_t acc[FA][FT] = {};  // rows of half 0, then of half 1
     V a[2][FA], b[2][FT];
-    int sa[2][FA], sb[2][FT];  // MXFP4: the scales of these fragments, one per lane
+    int sa[2][FA], sb[2][FT];  // MXFP4: the scales of both steps' fragments, of this stage and the next
     // read i (the token fragments first) of step st of a slot
     auto read = [&](int slot, int st, int i) {
         const LDS uint8_t *base = lds + slot * G::STAGE;
         if constexpr (P::mx) {
-            const LDS uint8_t *s = base + G::CODES + r16 * 8 + st * 4 + q4;
+            const LDS uint8_t *s = base + G::CODES + r16 * 8 + 2 * q4;
             const int f = i - FT;
-            if (i < FT) sb[st][i] = s[(TN + wt * (TM / WT) + i * 16) * 8];
-            else sa[st][f] = s[((f / G::FN) * (TN / 2) + wn * (TN / 2 / WN) + (f % G::FN) * 16) * 8];
+            if (st == 0 && i < FT) sb[1][i] = *reinterpret_cast<const LDS uint16_t *>(s + (TN + wt * (TM / WT) + i * 16) * 8);
+            if (st == 0 && i >= FT)
+                sa[1][f] = *reinterpret_cast<const LDS uint16_t *>(s + ((f / G::FN) * (TN / 2) + wn * (TN / 2 / WN) + (f % G::FN) * 16) * 8);
         }
         if (i < FT) {
             b[st][i] = __builtin_bit_cast(V, lds_ld16(base + fb[st] + i * 2048));
@@ -1130,7 +1141,9 @@ __global__ __launch_bounds__(WN * WT * 64) void k_linear_tile(P p, int tn, int t
 #pragma unroll
         for (int i = 0; i < NM; i++) {
             const int f = i / FT, g = f & 1 ? FT - 1 - i % FT : i % FT;
-            if constexpr (P::mx) acc[f][g] = mfma_mx(a[st][f], sa[st][f], b[st][g], sb[st][g], acc[f][g]);
+            if constexpr (P::mx)
+                acc[f][g] = st ? mfma_mx<1>(a[st][f], sa[0][f], b[st][g], sb[0][g], acc[f][g])
+                               : mfma_mx<0>(a[st][f], sa[0][f], b[st][g], sb[0][g], acc[f][g]);
             else acc[f][g] = mfma16v(a[st][f], b[st][g], acc[f][g]);
 #pragma unroll
             for (int j = i * NR / NM; j < (i + 1) * NR / NM; j++) read(slot, 1 - st, j);
@@ -1173,6 +1186,12 @@ __global__ __launch_bounds__(WN * WT * 64) void k_linear_tile(P p, int tn, int t
     int slot = 0;
     auto one_stage = [&](auto check, int s, uint4(&h)[G::CW]) {
         const int next = slot + 1 == NST ? 0 : slot + 1, last = slot == 0 ? NST - 1 : slot - 1;
+        if constexpr (P::mx) {
+#pragma unroll
+            for (int i = 0; i < FA; i++) sa[0][i] = sa[1][i];
+#pragma unroll
+            for (int i = 0; i < FT; i++) sb[0][i] = sb[1][i];
+        }
         __builtin_amdgcn_sched_barrier(0);
         part(check, 0, slot, 0, 0);
         // (every wave has read the last stage's slot by now: it is filled anew below)
@@ -1341,8 +1360,9 @@ __global__ __launch_bounds__(256, 2) void k_linear_pair(P p, int tn, int tt, int
 
     // copies: 16 rows of a weight quarter per wave (rows 16 wv + 8 j + lane / 8
     // of it: half a quarter each for either pair of waves), 8 of the tokens' next 32
-    const int l8 = lane >> 3, piece = (lane & 7) ^ (l8 >> 1);
-    const int ka[2] = {piece * 8, (piece ^ 4) * 8}, kx = (piece ^ (wv & 1 ? 4 : 0)) * 8;
+    const int l8 = lane >> 3, piece = (lane & 7) ^ (P::mx ? mx_place(l8 >> 1) : l8 >> 1);
+    constexpr int ODD = P::mx ? 6 : 4;  // (rows 8 on)
+    const int ka[2] = {piece * 8, (piece ^ ODD) * 8}, kx = (piece ^ (wv & 1 ? ODD : 0)) * 8;
     uint32_t va[2], vx[4];
 #pragma unroll
     for (int j = 0; j < 2; j++) {
@@ -1404,18 +1424,19 @@ __global__ __launch_bounds__(256, 2) void k_linear_pair(P p, int tn, int tt, int
     const int wn = wv >> 1, wt = wv & 1;
     int fo[2];
 #pragma unroll
-    for (int st = 0; st < 2; st++) fo[st] = r16 * 128 + (((st * 4 + q4) ^ (r16 >> 1)) << 4);
+    for (int st = 0; st < 2; st++)
+        fo[st] = r16 * 128 + ((P::mx ? (2 * q4 + st) ^ mx_place(r16 >> 1) : (st * 4 + q4) ^ (r16 >> 1)) << 4);
     const LDS uint8_t *fa = lds + wn * 4096, *fb = lds + G::B0 + wt * 8192;
-    const int fsa = G::QCODES + (wn * 32 + r16) * 8 + q4, fsb = G::BCODES + (wt * 64 + r16) * 8 + q4;
+    const int fsa = G::QCODES + (wn * 32 + r16) * 8 + 2 * q4, fsb = G::BCODES + (wt * 64 + r16) * 8 + 2 * q4;
     f32x4_t acc[4][2][4] = {};  // [quarter][16 rows][16 tokens]
     V a[2][2][2], b[2][4];      // [buffer][step][16 rows], [step][16 tokens]
-    int sa[2][2][2], sb[2][4];
+    int sa[2][2], sb[4];        // MXFP4: both steps' scales
     auto read_a = [&](int buf, int slot) {
 #pragma unroll
         for (int st = 0; st < 2; st++)
 #pragma unroll
             for (int f = 0; f < 2; f++) {
-                if constexpr (P::mx) sa[buf][st][f] = lds[slot * G::A + fsa + f * 128 + st * 4];
+                if (P::mx && st == 0) sa[buf][f] = *reinterpret_cast<const LDS uint16_t *>(lds + slot * G::A + fsa + f * 128);
                 a[buf][st][f] = __builtin_bit_cast(V, lds_ld16(fa + slot * G::A + fo[st] + f * 2048));
             }
     };
@@ -1424,7 +1445,7 @@ __global__ __launch_bounds__(256, 2) void k_linear_pair(P p, int tn, int tt, int
         for (int st = 0; st < 2; st++)
 #pragma unroll
             for (int g = 0; g < 4; g++) {
-                if constexpr (P::mx) sb[st][g] = lds[G::B0 + slot * G::B + fsb + g * 128 + st * 4];
+                if (P::mx && st == 0) sb[g] = *reinterpret_cast<const LDS uint16_t *>(lds + G::B0 + slot * G::B + fsb + g * 128);
                 b[st][g] = __builtin_bit_cast(V, lds_ld16(fb + slot * G::B + fo[st] + g * 2048));
             }
     };
@@ -1469,7 +1490,8 @@ __global__ __launch_bounds__(256, 2) void k_linear_pair(P p, int tn, int tt, int
             for (int i = 0; i < 16; i++) {
                 const int st = i >> 3, f = (i >> 2) & 1, g = f ? 3 - (i & 3) : i & 3;
                 if constexpr (P::mx)
-                    acc[q][f][g] = mfma_mx(a[q & 1][st][f], sa[q & 1][st][f], b[st][g], sb[st][g], acc[q][f][g]);
+                    acc[q][f][g] = st ? mfma_mx<1>(a[q & 1][st][f], sa[q & 1][f], b[st][g], sb[g], acc[q][f][g])
+                                      : mfma_mx<0>(a[q & 1][st][f], sa[q & 1][f], b[st][g], sb[g], acc[q][f][g]);
                 else acc[q][f][g] = mfma16v(a[q & 1][st][f], b[st][g], acc[q][f][g]);
                 if (i % 4 == 1 && i / 4 < G::C)
                     copy(i / 4, (q + 1) & 3, q == 3 ? s + 2 : s + 1, slot, true, q == 0 ? s + 1 : s + 2);
@@ -1573,8 +1595,8 @@ __global__ __launch_bounds__(kFewWaves * 64) void k_linear_few(P p)
     const __amdgpu_buffer_rsrc_t rx =
         rows_rsrc(reinterpret_cast<const uint16_t *>(p.x) + (size_t)t0 * p.ldx, min(8 * XP, p.M - t0), p.ldx, p.K);
     uint32_t cw[2], cx[XP];
-    const int piece = (lane & 7) ^ (l8 >> 1);
-    const int kc[2] = {piece * 8, (piece ^ 4) * 8};
+    const int piece = (lane & 7) ^ (P::mx ? mx_place(l8 >> 1) : l8 >> 1);
+    const int kc[2] = {piece * 8, (piece ^ (P::mx ? 6 : 4)) * 8};
 #pragma unroll
     for (int j = 0; j < 2; j++) cw[j] = (uint32_t)((8 * j + l8) * p.ldw * 2) + (kc[j] + s0 * 64) * 2;
 #pragma unroll
@@ -1620,7 +1642,8 @@ __global__ __launch_bounds__(kFewWaves * 64) void k_linear_few(P p)
     };
     int fo[2];
 #pragma unroll
-    for (int st = 0; st < 2; st++) fo[st] = r16 * 128 + (((st * 4 + q4) ^ (r16 >> 1)) << 4);
+    for (int st = 0; st < 2; st++)
+        fo[st] = r16 * 128 + ((P::mx ? (2 * q4 + st) ^ mx_place(r16 >> 1) : (st * 4 + q4) ^ (r16 >> 1)) << 4);
     // (eight tokens: the other half of the tile repeats them)
     const int fx = XP == 1 ? fo[0] & 1023 : fo[0], fx1 = XP == 1 ? fo[1] & 1023 : fo[1];
     f32x4_t acc[G::NR][G::MT] = {};
@@ -1631,15 +1654,16 @@ __global__ __launch_bounds__(kFewWaves * 64) void k_linear_few(P p)
         wait_copies<(NST - 1) * G::CW>();
         const LDS uint8_t *base = ring + slot * G::STAGE;
         V a[2][G::NR], b[2][G::MT];
-        int sa[2][G::NR], sb[2][G::MT];
+        int sa[G::NR], sb[G::MT];  // MXFP4: both steps' scales
 #pragma unroll
         for (int st = 0; st < 2; st++) {
-            if constexpr (P::mx) {
-                const LDS uint8_t *s = base + G::CODES + r16 * 8 + st * 4 + q4;
+            if (P::mx && st == 0) {
+                const LDS uint8_t *s = base + G::CODES + r16 * 8 + 2 * q4;
 #pragma unroll
-                for (int i = 0; i < G::NR; i++) sa[st][i] = s[i * 256];
+                for (int i = 0; i < G::NR; i++) sa[i] = *reinterpret_cast<const LDS uint16_t *>(s + i * 256);
 #pragma unroll
-                for (int m = 0; m < G::MT; m++) sb[st][m] = (XP == 1 ? s - (r16 & 8) * 8 : s)[G::NR * 256 + m * 128];
+                for (int m = 0; m < G::MT; m++)
+                    sb[m] = *reinterpret_cast<const LDS uint16_t *>((XP == 1 ? s - (r16 & 8) * 8 : s) + G::NR * 256 + m * 128);
             }
 #pragma unroll
             for (int i = 0; i < G::NR; i++) a[st][i] = __builtin_bit_cast(V, lds_ld16(base + fo[st] + i * 2048));
@@ -1655,7 +1679,9 @@ __global__ __launch_bounds__(kFewWaves * 64) void k_linear_few(P p)
             for (int i = 0; i < G::NR; i++)
 #pragma unroll
                 for (int m = 0; m < G::MT; m++) {
-                    if constexpr (P::mx) acc[i][m] = mfma_mx(a[st][i], sa[st][i], b[st][m], sb[st][m], acc[i][m]);
+                    if constexpr (P::mx)
+                        acc[i][m] = st ? mfma_mx<1>(a[st][i], sa[i], b[st][m], sb[m], acc[i][m])
+                                       : mfma_mx<0>(a[st][i], sa[i], b[st][m], sb[m], acc[i][m]);
                     else acc[i][m] = mfma16v(a[st][i], b[st][m], acc[i][m]);
                 }
         slot = slot + 1 == NST ? 0 : slot + 1;

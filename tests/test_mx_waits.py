@@ -15,7 +15,7 @@ SOURCE = open(os.path.join(os.path.dirname(moe.__file__), "csrc", "linear_dev.h"
 UNIT = re.compile(r"unit\(D(\d)\{\}, r(\w+), s(\w+), (?:BUF \+ )?(\w+), (\w+)\);")
 STEP = re.compile(r"turn\(f([ab]), (-?)BUF\)|phase\(check, D(\d)\{\}, r(\w+), s(\w+), (?:BUF \+ )?(\w+), (\w+), .*?"
                   r"read([AB])\(\w+, (\w+), i\)")
-COPIES, READS = 5, 2     # per unit and wave (four of codes, one of scales); per fragment (and its scale)
+COPIES, READS = 5, 12    # per unit and wave: four of codes, one of scales; of a half: eight fragments, four pairs of scales
 
 
 class Wave:
@@ -58,9 +58,10 @@ def test_mx_big():
     wave.wait(int(waits[0]), 0)
     wave.barrier()
     for unit in ("A0", "B0"):
-        wave.read((unit, 0), 0, 8 * READS)
+        wave.read((unit, 0), 0, READS)
     wave.wait(int(waits[1]), 0)
     (n, lds), = re.findall(r"wait_copies<(\d+), (\d+)>\(\);\s*barrier\(\);", head)
+    assert "if (i < 4) h.s[i] =" in SOURCE[SOURCE.index("void k_mx_big("):]
     assert "if (i % 4 == 0) read(i >> 2);" in head and "if (i % 6 == 2 && i < 30) copy(check, d, r, s, at, b, i / 6);" in head
     steps = STEP.findall(stages)
     assert sum(not s[0] for s in steps) == 8
@@ -79,10 +80,10 @@ def test_mx_big():
             assert place != source
             now = max(w for p, w in wave.copies if p == source)
             wave.copy(place, stage, COPIES)
-            wave.read(source, now, 8 * READS)
+            wave.read(source, now, READS)
         assert buffer == {"A": 0, "B": 0}
     # what a phase reads is the stage that the next one multiplies
-    read = [w for p, w in wave.reads if p[0] == "A1"][::8 * READS]
+    read = [w for p, w in wave.reads if p[0] == "A1"][::READS]
     assert read == list(range(len(read)))
 
 
