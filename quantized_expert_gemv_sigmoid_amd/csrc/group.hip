@@ -14,6 +14,9 @@ namespace {
 // same call always gives the same places.  Each wave owns a run of choices and
 // goes through it 64 at a time; a choice's rank among the wave's is what the
 // wave has counted of its expert so far plus the lower lanes that chose it too.
+// Up to 1024 choices in one launch (16 of 896 experts 3.4 us, a chain of loads
+// and barriers; 16 waves for them took 6.9), more in two: 32768 of 64 experts 5
+// and 7 us, 32 blocks of 1024 (8 of 4096: 6.5 and 13).
 constexpr int kGroupWaves = 16;
 constexpr int kGroupThreads = kGroupWaves * 64;
 
@@ -187,7 +190,10 @@ __device__ __forceinline__ void to_f32(const Raw8 &r, int type, float (&v)[8])
 
 // A thread adds eight columns of a token's rows, in the order of its choices,
 // fp32 throughout; YT: the rows' type.  B rows are on the way at once; a choice
-// without a row reads one that is there and adds nothing.
+// without a row reads one that is there and adds nothing.  Bound by memory: 4096
+// tokens of 8 rows of 2048 bf16 with a residual 29 us (5400 GB/s; four rows on
+// the way and a branch for each 45), of fp32 rows 54; one token of 16 5 us, a
+// chain of three loads.
 template <int YT, int B>
 __global__ __launch_bounds__(256) void k_group_combine(CombineParams p)
 {

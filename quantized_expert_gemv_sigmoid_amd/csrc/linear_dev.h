@@ -1,14 +1,19 @@
 // Dense product with its epilogue (moe_linear):
 //   out[t][n] = act(sum_k x[t][k] w[n][k] + bias[n]) + residual[t][n],
-// or act of two such sums (w and w_up) for the gated activations.
+// or act of two such sums (w and w_up) for the gated activations; the same on
+// MXFP4 operands (moe_mx_linear), and with weights of its own for each group of
+// rows (moe_grouped_linear).
 //
 // Every kernel multiplies D[n][t] = w x^T on the matrix cores with fp32 sums:
 // the weights are the A operand, so a lane ends with four consecutive n of
 // one token.  K comes in stages of 64 into LDS rows of 128 bytes, their
 // 16-byte pieces permuted (piece ^ row / 2) so that fragment reads touch every
-// bank alike.  Four kernels, by what bounds them (which call takes which:
+// bank alike.  The kernels, by what bounds them (which call takes which:
 // linear.hip):
 //   k_linear_big   the matrix cores: 256 x 256 tiles
+//   k_mx_big       the same on MXFP4 operands
+//   k_linear_pair  power and the ends of a block: 256 x 128 tiles, two blocks to
+//                  a CU (groups, MXFP4)
 //   k_linear_tile  LDS reads and latency: 64 x 32 to 128 x 128 tiles
 //   k_linear_few   the weights' way from memory, each row read once: 16 rows
 //                  x 8 to 32 tokens
@@ -779,6 +784,14 @@ constexpr int kMxLds = 4 * kBigWave > 8 * kMxUnit ? 4 * kBigWave : 8 * kMxUnit;
 // bytes of a row are 256 codes, and one product takes 128 of them in the
 // cycles of a 16-bit one's 32.  The 8 scales of a row and stage are copied
 // behind their unit; a lane's products take one byte each, read from there.
+// Measured: 4096 x 7168 x 4096, one turn of tiles, 63 us (3790 TFLOP/s; a stage
+// 1.65 us, and 17 for the launch, the first copies and the epilogue), 4096 x
+// 7168 x 7168 112-136, 8192^3 270-296 (4080-3710 TFLOP/s).  Bound by power where
+// K is long: the same call on zeros takes 3/4 of the time (4096 x 14336 x 4096 94
+// us, 126 on random codes), products of random codes from registers alone reach
+// 6000 to 7500 TFLOP/s, of zeros 9600.  Both steps' scales in one read (a byte
+// read each: 3 to 4% more); copies of scales that lay side by side would save
+// another 4%.
 template <bool F16, bool GATED>
 __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(1, 1))) void k_mx_big(MxParams p, int tn, int tt, int ksplit)
 {
@@ -987,7 +1000,10 @@ __device__ __forceinline__ f32x4_t mfma_mx(V a, int sa, V b, int sb, f32x4_t c)
 // 333 x 1117 x 2049 12.8 and 13.9 us (21, 21), 2048 x 1117 x 2049 38 and 41
 // (27, 27), 2048 x 3585 x 3587 86 and 116 (74, 89).
 // MXFP4 rows: 128 bytes are 256 codes, a stage of the same bytes, and each wave
-// copies 32 rows' scales of it, 8 bytes a row, behind them.
+// copies 32 rows' scales of it, 8 bytes a row, behind them: 512 x 3584 x 7168 14.2
+// us (128 x 128), 200 x 1120 x 2049 7.2 (64 x 32).  Groups: 512 rows of 64 groups x
+// 2048 x 3584 (64 x 32) 147 us, 6400 GB/s of weights, one token's eight of 128
+// experts x 3584 x 2 x 2048 36 us.
 template <int TN, int TM, int WN, int WT, int NST, bool MX>
 struct Tile {
     static constexpr int NW = WN * WT, THREADS = NW * 64;
@@ -1324,6 +1340,15 @@ __global__ __launch_bounds__(256) void k_linear_join(LinearParams p)
 // stages of 128 bytes a row; a stage's weights come in four quarters of 64 rows
 // (32 for either pair of waves), each multiplied with the whole stage's tokens
 // in a phase of its own: quarters in a ring of five, tokens in one of two.
+// Measured beside 256 x 256 tiles, one block to a CU: 16384 rows of 64 ragged
+// groups x 3584 x 2 x 2048, SiTU, MXFP4 250 us (335); 32768 of 64 x 2048 x 2 x
+// 1408, SwiGLU, bf16 400-430 (410-440), 16384 rows of 128 groups x 2048 x 2 x
+// 1024 247 (290); one group of 4096 x 8192 x 4096 bf16 207 (1330 TFLOP/s).  With
+// long K they are 10% behind (4096 x 7168 x 7168 MXFP4 127, 112): a wave reads
+// 1.5 times the LDS bytes per product.  Power again: the SwiGLU call takes 352
+// on zeros.  Six quarters in the ring, a higher wave priority at the products,
+// products kept in the order they are written in, and products skipped for
+// tokens past a group's end were equal or 3 to 5% slower.
 template <bool MX>
 struct Pair {
     static constexpr int QROWS = 64, TOKENS = 128, NA = 5, NB = 2;

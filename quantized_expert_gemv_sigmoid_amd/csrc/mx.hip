@@ -6,6 +6,12 @@
 // -127; its values over 2^e are rounded to E2M1.  The exponent is read off the
 // largest magnitude's bits and the quotients are exact, so nothing is rounded
 // but the codes.
+//
+// Both kernels are bound by memory: 28672 x 3584 bf16 quantised 42-53 us (260 MB,
+// 6150-4900 GB/s with inputs in turn), read back 42-48; fp32 84 and 84; one row
+// of 7168 2.0 and 2.5 (a launch).  Two quarters of blocks per thread on the way
+// at once: one is 5% slower to read back (50.2 us), four 5% slower for short rows
+// (60000 x 300: 11.3 us, 10.5 with two).
 #include <algorithm>
 #include <type_traits>
 
