@@ -265,7 +265,12 @@ int64_t group_per(int64_t R) { return std::max<int64_t>(1024, (R + 63) / 64); }
 
 }  // namespace
 
-size_t group_workspace(int64_t R, int E) { return R > group_per(R) ? (size_t)((R + group_per(R) - 1) / group_per(R)) * E * 4 : 256; }
+// (at least what a call of fewer choices takes)
+size_t group_workspace(int64_t R, int E)
+{
+    const int64_t blocks = (R + group_per(R) - 1) / group_per(R);
+    return blocks > 1 ? std::max<size_t>(256, (size_t)blocks * E * 4) : 256;
+}
 
 // (R: 2^26 at most)
 hipError_t launch_group(const int32_t *ids, int64_t R, int k, int E, int32_t *offsets, int32_t *tokens, int32_t *places,

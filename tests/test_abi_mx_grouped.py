@@ -169,6 +169,12 @@ def test_group_and_combine_refused(L):  # noqa: F811
         assert combine(**kw) == moe.EUNSUPPORTED, kw
 
 
+@pytest.mark.parametrize("E", [1, 31, 64, 1024])
+def test_a_group_workspace_serves_fewer_tokens(L, E):  # noqa: F811
+    need = [L.moe_group_workspace_bytes(T, 4, E) for T in (0, 1, 255, 256, 257, 300, 1000, 16384, 16385, 16500, 30000, 1 << 20)]
+    assert need == sorted(need) and need[0] >= 256
+
+
 # ------------------------------------------------------------------ the binding
 
 def u8(*shape, device="cpu"):
