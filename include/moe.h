@@ -519,7 +519,8 @@ moe_status moe_mx_linear(const moe_mx_linear_desc *desc, const uint8_t *x, int64
  *   tokens[T k]: the token of each row (the places from offsets[n_experts] on
  *   are left as they are);
  *   places[T][k]: the row of each choice, -1 for none.
- * n_experts up to 1024, k up to 64.  Workspace as moe_linear's.
+ * n_experts up to 1024, k up to 64.  Workspace as moe_linear's.  The outputs
+ * must not overlap ids or each other.
  */
 size_t moe_group_workspace_bytes(int32_t max_tokens, int32_t top_k, int32_t n_experts);
 moe_status moe_group(const int32_t *ids, int32_t T, int32_t top_k, int32_t n_experts, int32_t *offsets, int32_t *tokens,
@@ -545,8 +546,8 @@ typedef struct {
     const void *bias, *bias_up;  /* [n_groups][n_out], or NULL                   */
 } moe_grouped_desc;
 
-/* The kernel that moe_grouped_linear takes for R >= 1 rows: a moe_linear_path
- * + 256. */
+/* The kernel that moe_grouped_linear takes for R >= 1 rows of as many rows of
+ * x: a moe_linear_path + 256. */
 int32_t moe_grouped_path_for(const moe_grouped_desc *desc, const void *x, int64_t ldx, int32_t R);
 
 /*
@@ -560,7 +561,9 @@ int32_t moe_grouped_path_for(const moe_grouped_desc *desc, const void *x, int64_
  * are read on the device, so the call needs no synchronisation behind moe_group.
  *
  * 0 <= R <= 2^24; ldx, ldw, ldo up to 2^22 (MXFP4: ldx, ldw up to 2^23, ldxs,
- * ldw_s to 2^22); with `rows`, x's rows lie within 2 GiB.  MXFP4: n_in a multiple
+ * ldw_s to 2^22); with `rows`, x's rows lie within 2 GiB; a launch holds fewer
+ * than 2^32 threads (n_out (R / 128 + n_groups) below 2^28 always does;
+ * MOE_EUNSUPPORTED where none can).  MXFP4: n_in a multiple
  * of 128, rows of codes at multiples of 16 bytes, rows of scales at multiples
  * of 4 (MOE_EUNSUPPORTED for n_in and the scales).  16-bit elements need their
  * own alignment only; rows at multiples of 16 bytes, n_in of 8, take the

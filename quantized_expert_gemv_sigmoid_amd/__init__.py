@@ -689,7 +689,7 @@ def mx_linear_workspace(desc: MxLinearDesc, max_tokens: int, device="cuda"):
 
 
 def mx_linear_path_for(desc: MxLinearDesc, T: int) -> tuple:
-    """(kernel, parts of n_in) that `mx_linear` takes for T tokens: one of LINEAR_ROWS16X8 .. TILE256X256."""
+    """(kernel, parts of n_in) that `mx_linear` takes for T tokens: one of LINEAR_ROWS16X8 .. TILE256X128."""
     r = int(lib().moe_mx_linear_path_for(ctypes.byref(desc), T))
     if r < 0:
         raise MoeError(r, "moe_mx_linear_path_for")
@@ -770,7 +770,7 @@ def _grouped_x(desc: GroupedDesc, x, rows: int, what: str = "x") -> int:
 
 
 def grouped_path_for(desc: GroupedDesc, x, R: int) -> int:
-    """The kernel that `grouped_linear` takes for R rows: one of LINEAR_ROWS16X8 .. TILE256X256."""
+    """The kernel that `grouped_linear` takes for R rows of x: one of LINEAR_TILE64X32 .. TILE256X128."""
     r = int(lib().moe_grouped_path_for(ctypes.byref(desc), x.data_ptr(), _grouped_x(desc, x, x.shape[0]), R))
     if r < 0:
         raise MoeError(r, "moe_grouped_path_for")

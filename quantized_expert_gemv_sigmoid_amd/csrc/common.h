@@ -613,8 +613,8 @@ void launch_grouped_bf16(const GroupedParams &p, const LinearPlan &c, hipStream_
 void launch_grouped_f16(const GroupedParams &p, const LinearPlan &c, hipStream_t st);
 void launch_grouped_mx_bf16(const GroupedMxParams &p, const LinearPlan &c, hipStream_t st);
 void launch_grouped_mx_f16(const GroupedMxParams &p, const LinearPlan &c, hipStream_t st);
-hipError_t launch_grouped(const GroupedParams &p, bool f16, hipStream_t st);
-hipError_t launch_grouped_mx(const GroupedMxParams &p, bool f16, hipStream_t st);
+hipError_t launch_grouped(const GroupedParams &p, const LinearPlan &c, bool f16, hipStream_t st);
+hipError_t launch_grouped_mx(const GroupedMxParams &p, const LinearPlan &c, bool f16, hipStream_t st);
 
 size_t group_workspace(int64_t R, int E);
 hipError_t launch_group(const int32_t *ids, int64_t R, int k, int E, int32_t *offsets, int32_t *tokens, int32_t *places,

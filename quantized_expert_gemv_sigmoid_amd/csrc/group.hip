@@ -48,6 +48,7 @@ __device__ __forceinline__ void count_choices(const int32_t *ids, int a, int b, 
         const bool on = (uint32_t)id < (uint32_t)E;
         const uint64_t same = same_lanes(id, on);
         if (on && (same & ((1ull << lane) - 1)) == 0) mine[id] += __popcll(same);  // (one lane per expert)
+        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
     }
 }
 
@@ -130,13 +131,12 @@ __global__ __launch_bounds__(kGroupThreads) void k_group_place(const int32_t *id
         const int id = c < b0 ? ids[c] : -1;
         const bool on = (uint32_t)id < (uint32_t)E;
         const uint64_t same = same_lanes(id, on), lower = same & ((1ull << lane) - 1);
-        int place = -1;
-        if (on) {
-            const int first = mine[id];
-            place = first + __popcll(lower);
-            if (lower == 0) mine[id] = first + __popcll(same);
-            tokens[place] = (int)((uint32_t)c / (uint32_t)k);
-        }
+        // (all lanes read before one of them writes, for the next 64 to read)
+        const int first = on ? mine[id] : 0, place = on ? first + __popcll(lower) : -1;
+        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+        if (on && lower == 0) mine[id] = first + __popcll(same);
+        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+        if (on) tokens[place] = (int)((uint32_t)c / (uint32_t)k);
         if (c < b0) places[c] = place;
     }
 }

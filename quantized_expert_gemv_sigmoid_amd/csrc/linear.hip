@@ -179,14 +179,14 @@ namespace {
 // A kernel's tile, and the time in ns of a stage of 64 of K (256 of codes) and
 // of a block's start and end, per block and CU.
 struct GroupedKind {
-    int kind, rows, tokens, each_ns, ends_ns;
+    int kind, rows, tokens, threads, each_ns, ends_ns;
     bool any;
 };
 constexpr GroupedKind kGroupedKinds[] = {
-    {kTile64x32, 64, 32, 130, 2350, false},    {kTile64x64, 64, 64, 180, 2750, false},
-    {kTile128x64, 128, 64, 310, 4500, false},  {kTile128x128, 128, 128, 500, 6000, false},
-    {kTile256x128, 256, 128, 950, 5000, false}, {kAny64x32, 64, 32, 290, 1900, true},
-    {kAny64x64, 64, 64, 400, 3000, true},      {kAny128x128, 128, 128, 950, 6500, true},
+    {kTile64x32, 64, 32, 256, 130, 2350, false},    {kTile64x64, 64, 64, 256, 180, 2750, false},
+    {kTile128x64, 128, 64, 512, 310, 4500, false},  {kTile128x128, 128, 128, 512, 500, 6000, false},
+    {kTile256x128, 256, 128, 256, 950, 5000, false}, {kAny64x32, 64, 32, 256, 290, 1900, true},
+    {kAny64x64, 64, 64, 256, 400, 3000, true},      {kAny128x128, 128, 128, 512, 950, 6500, true},
 };
 
 }  // namespace
@@ -201,19 +201,20 @@ constexpr GroupedKind kGroupedKinds[] = {
 // of 64 x 2048 x 3584 64 x 32 147 us, 256 x 128 168; 4096 of 64 x 2048 x 2 x 1408
 // 256 x 128 171, 128 x 128 184, 64 x 32 232; 128 of 8 x 4096 x 4096 64 x 64 43,
 // 64 x 32 51; 16 of 896 x 1024 x 2 x 512 64 x 32 8.5, 64 x 64 9.9.  The kernels of
-// 16 rows lost at every size (16 of 896: 13 us).
+// 16 rows lost at every size (16 of 896: 13 us).  Kind -1: too large for any.
 LinearPlan grouped_plan(const GroupedParams &p, bool mx)
 {
     const bool any = !mx && !(pieces(p) && p.wstride % 8 == 0);
     const int m = p.w_up ? 2 : 1, stages = (p.K + 63) / 64;
     const double active = p.groups * (1.0 - std::exp(-(double)p.M / p.groups));
     const double weights = 2.0 * m * active * p.N * p.K;
-    LinearPlan best = {any ? kAny128x128 : kTile256x128, 1};
+    LinearPlan best = {-1, 1};
     double least = 1e30;
     for (const GroupedKind &k : kGroupedKinds) {
         if (k.any != any) continue;
         const double columns = std::ceil((double)p.N * m / k.rows);
-        if (columns * ((double)p.M / k.tokens + p.groups) > 1e9) continue;
+        // (a launch holds fewer than 2^32 threads)
+        if (columns * ((double)p.M / k.tokens + std::min(p.groups, p.M)) * k.threads > 4.2e9) continue;
         const double full = columns * std::max(active, (double)p.M / k.tokens + 0.5 * active) / kCus;
         const double work = std::max(1.0, full) * k.each_ns * stages + full * k.ends_ns;
         const double ns = std::max(work, weights / 5600.0) + 0.1 * work;
@@ -225,21 +226,19 @@ LinearPlan grouped_plan(const GroupedParams &p, bool mx)
     return best;
 }
 
-hipError_t launch_grouped(const GroupedParams &params, bool f16, hipStream_t st)
+hipError_t launch_grouped(const GroupedParams &params, const LinearPlan &c, bool f16, hipStream_t st)
 {
     GroupedParams p = params;
     p.vec = fours(p);
-    const LinearPlan c = grouped_plan(p, false);
     if (f16) launch_grouped_f16(p, c, st);
     else launch_grouped_bf16(p, c, st);
     return hipGetLastError();
 }
 
-hipError_t launch_grouped_mx(const GroupedMxParams &params, bool f16, hipStream_t st)
+hipError_t launch_grouped_mx(const GroupedMxParams &params, const LinearPlan &c, bool f16, hipStream_t st)
 {
     GroupedMxParams p = params;
     p.vec = fours(p);
-    const LinearPlan c = grouped_plan(p, true);
     if (f16) launch_grouped_mx_f16(p, c, st);
     else launch_grouped_mx_bf16(p, c, st);
     return hipGetLastError();

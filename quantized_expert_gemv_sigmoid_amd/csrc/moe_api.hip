@@ -1056,7 +1056,7 @@ int32_t moe_grouped_path_for(const moe_grouped_desc *desc, const void *x, int64_
     const moe_status s2 = grouped_params(desc, x, xs, ldx, desc->n_in / 32, R, nullptr, &offsets, R, p);
     if (s2 != MOE_OK) return s2;
     const moe::LinearPlan c = moe::grouped_plan(p, desc->operands == MOE_MXFP4);
-    return c.kind + 256 * c.ksplit;
+    return c.kind < 0 ? MOE_EUNSUPPORTED : c.kind + 256 * c.ksplit;
 }
 
 moe_status moe_grouped_linear(const moe_grouped_desc *desc, const void *x, int64_t ldx, const uint8_t *x_s, int64_t ldxs,
@@ -1079,9 +1079,11 @@ moe_status moe_grouped_linear(const moe_grouped_desc *desc, const void *x, int64
     p.out_half = out_mode != MOE_OUT_F32 ? out_half : nullptr;
     p.out_f32 = out_mode != MOE_OUT_BF16 ? out_f32 : nullptr;
     p.ldo = ldo;
+    const moe::LinearPlan c = moe::grouped_plan(p, desc->operands == MOE_MXFP4);
+    if (c.kind < 0) return MOE_EUNSUPPORTED;
     (void)hipGetLastError();
-    if (desc->operands == MOE_MXFP4) MOE_TRY(moe::launch_grouped_mx(p, desc->type == MOE_F16, (hipStream_t)stream));
-    else MOE_TRY(moe::launch_grouped(p, desc->type == MOE_F16, (hipStream_t)stream));
+    if (desc->operands == MOE_MXFP4) MOE_TRY(moe::launch_grouped_mx(p, c, desc->type == MOE_F16, (hipStream_t)stream));
+    else MOE_TRY(moe::launch_grouped(p, c, desc->type == MOE_F16, (hipStream_t)stream));
     return MOE_OK;
 }
 

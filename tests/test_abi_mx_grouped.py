@@ -127,6 +127,26 @@ def test_grouped_call_refused(L):  # noqa: F811
         assert call_grouped(L, m, **kw) == moe.EUNSUPPORTED, kw
 
 
+
+@pytest.mark.parametrize("base", [GROUPED, GROUPED_MX])
+@pytest.mark.parametrize("gated", [0, 1])
+def test_groups_of_more_threads_than_a_launch_holds_are_refused(L, base, gated):  # noqa: F811
+    up = dict(act=moe.LINEAR_SWIGLU, w_up=FAKE, w_up_s=FAKE if base is GROUPED_MX else None) if gated else {}
+    ld = 320 if base is GROUPED_MX else 640
+
+    d = filled(moe.GroupedDesc, base, {**up, "n_out": 1 << 20, "n_groups": 1024, "group_w": 0, "group_w_s": 0})
+    assert L.moe_grouped_path_for(ctypes.byref(d), FAKE, ld, 1 << 24) == moe.EUNSUPPORTED
+    assert call_grouped(L, d, R=1 << 24, x_rows=1 << 24, ldo=1 << 20) == moe.EUNSUPPORTED
+    # (64 x 32 tiles, with the least idle rows, would be 2^25.6 blocks of 256)
+    assert L.moe_grouped_path_for(ctypes.byref(d), FAKE, ld, 65536) == moe.LINEAR_TILE256X128 + 256
+    if base is GROUPED:
+        d.n_out = 1 << 17
+        r = L.moe_grouped_path_for(ctypes.byref(d), FAKE + 2, ld, 1 << 17)
+        assert r >= 0 and r % 256 in (moe.LINEAR_ANY64X32, moe.LINEAR_ANY64X64, moe.LINEAR_ANY128X128)
+        d.n_out = 1 << 20
+        assert L.moe_grouped_path_for(ctypes.byref(d), FAKE + 2, ld, 1 << 17) == moe.EUNSUPPORTED
+
+
 def test_mx_rows_refused(L):  # noqa: F811
     def quantize(x=FAKE, type=moe.BF16, ldx=70, T=3, n=70, rule=0, c=FAKE, ldc=48, s=FAKE, lds=3):
         return L.moe_mx_quantize(x, type, ldx, T, n, rule, c, ldc, s, lds, None)
