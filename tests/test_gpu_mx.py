@@ -141,8 +141,7 @@ def test_no_rows_and_a_few_of_them():
     assert (s[:3] == 125).all() and (c[:3] == 0x66).all() and (c[3] == 9).all() and (s[3] == 9).all()
 
 
-def test_rows_of_more_than_a_launch():
-    """2^30 eighths of blocks are one launch's: more rows than that of one value each."""
+def test_a_million_rows_of_one_value():
     T = (1 << 20)
     x = power(torch.arange(T, device="cuda") % 40 - 20)[:, None].bfloat16()
     c, s = quantize(x, "floor")
