@@ -546,8 +546,9 @@ typedef struct {
     const void *bias, *bias_up;  /* [n_groups][n_out], or NULL                   */
 } moe_grouped_desc;
 
-/* The kernel that moe_grouped_linear takes for R >= 1 rows of as many rows of
- * x: a moe_linear_path + 256. */
+/* The kernel that moe_grouped_linear takes for R >= 1 rows from an x at this
+ * address with this row distance (n_in where x has one row): a moe_linear_path
+ * + 256. */
 int32_t moe_grouped_path_for(const moe_grouped_desc *desc, const void *x, int64_t ldx, int32_t R);
 
 /*

@@ -769,9 +769,11 @@ def _grouped_x(desc: GroupedDesc, x, rows: int, what: str = "x") -> int:
     return _rows(x, rows, desc.n_in, what)
 
 
-def grouped_path_for(desc: GroupedDesc, x, R: int) -> int:
-    """The kernel that `grouped_linear` takes for R rows of x: one of LINEAR_TILE64X32 .. TILE256X128."""
-    r = int(lib().moe_grouped_path_for(ctypes.byref(desc), x.data_ptr(), _grouped_x(desc, x, x.shape[0]), R))
+def grouped_path_for(desc: GroupedDesc, x, R: int, rows=None) -> int:
+    """The kernel that `grouped_linear` takes for R rows of x, gathered by `rows` where that is given: one of
+    LINEAR_TILE64X32 .. TILE256X128."""
+    ldx = _grouped_x(desc, x, x.shape[0] if rows is not None else min(R, x.shape[0]))
+    r = int(lib().moe_grouped_path_for(ctypes.byref(desc), x.data_ptr(), ldx, R))
     if r < 0:
         raise MoeError(r, "moe_grouped_path_for")
     return r % 256

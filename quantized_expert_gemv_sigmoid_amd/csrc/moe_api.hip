@@ -1053,7 +1053,9 @@ int32_t moe_grouped_path_for(const moe_grouped_desc *desc, const void *x, int64_
     const int32_t offsets = 0;
     // (scales: any aligned address, none is read)
     const uint8_t *xs = desc->operands == MOE_MXFP4 ? reinterpret_cast<const uint8_t *>(&offsets) : nullptr;
-    const moe_status s2 = grouped_params(desc, x, xs, ldx, desc->n_in / 32, R, nullptr, &offsets, R, p);
+    // (a gathered row comes from among others, so that a distance that rows can have counts for one row too)
+    const int32_t x_rows = R == 1 && desc->operands != MOE_MXFP4 && ldx >= desc->n_in ? 2 : R;
+    const moe_status s2 = grouped_params(desc, x, xs, ldx, desc->n_in / 32, x_rows, nullptr, &offsets, R, p);
     if (s2 != MOE_OK) return s2;
     const moe::LinearPlan c = moe::grouped_plan(p, desc->operands == MOE_MXFP4);
     return c.kind < 0 ? MOE_EUNSUPPORTED : c.kind + 256 * c.ksplit;
