@@ -449,6 +449,13 @@ def _flat(t, n: int, dtype, what: str):
     return t.data_ptr()
 
 
+def _choices(t, T: int, k: int, dtype, what: str):
+    """_flat of T rows of k choices: a table of several rows is of that width."""
+    if t is not None and T > 1 and len(t.shape) == 2 and t.shape[1] != k:
+        raise MoeError(EINVAL, f"{what}: {T} rows of {k} values wanted, got {tuple(t.shape)}")
+    return _flat(t, T * k, dtype, what)
+
+
 def _same_device(desc, first, *others) -> None:
     """The tensors of a call lie on one device, and those of the descriptor (desc.device, where known) too."""
     i = first.get_device()
@@ -823,7 +830,7 @@ def group(ids, T: int, n_experts: int, offsets, tokens, places, ws, stream=None)
     wp, wn = _ws(ws)
     _check(_call(ids, stream, lib().moe_group, _flat(ids, T * k, i32, "ids"), T, k, n_experts,
                  _flat(offsets, n_experts + 1, i32, "offsets"), _flat(tokens, T * k, i32, "tokens"),
-                 _flat(places, T * k, i32, "places"), wp, wn), "moe_group")
+                 _choices(places, T, k, i32, "places"), wp, wn), "moe_group")
 
 
 def combine(y, R: int, places, weights, T: int, out, residual=None, stream=None) -> None:
@@ -838,5 +845,5 @@ def combine(y, R: int, places, weights, T: int, out, residual=None, stream=None)
     rt = F32 if residual is None else _type_of(residual)
     rp, ldr = _residual(residual, T, n, rt)
     _check(_call(y, stream, lib().moe_combine, y.data_ptr(), yt, _rows(y, R, n, "y"), R, _flat(places, T * k, _torch.int32, "places"),
-                 _flat(weights, T * k, _torch.float32, "weights"), T, k, n, rp, rt, ldr, out.data_ptr(), ot,
+                 _choices(weights, T, k, _torch.float32, "weights"), T, k, n, rp, rt, ldr, out.data_ptr(), ot,
                  _rows(out, T, n, "out")), "moe_combine")
