@@ -49,3 +49,15 @@ def test_binding():
     assert moe.grouped_path_for(d, x, 1) not in ANY
     assert moe.grouped_path_for(d, x[:1], 9, rows=rows) not in ANY
     assert moe.grouped_path_for(d, x[:1], 1, rows=rows) not in ANY
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("row", [0, 3, 4, -1, 5])
+def test_a_gathered_row_of_several(row):
+    import test_gpu_grouped as t
+    s = t.make(3, 1, 640, 40, gather=5, padx=5, whole=True, bias=torch.float32, seed=3)
+    s["rows"][0] = row
+    assert moe.grouped_path_for(t.descriptor(s), s["x"], 1, rows=s["rows"]) in ANY
+    f = t.call(s)[1]
+    a, b = t.covered(s)
+    assert b - a == 1 and torch.equal(f[a:b].double(), t.reference(s)[0][a:b])
