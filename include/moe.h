@@ -511,6 +511,9 @@ moe_status moe_mx_linear(const moe_mx_linear_desc *desc, const uint8_t *x, int64
  * choices of a routing sorted by expert (moe_group), the products of each
  * expert's rows with its weights (moe_grouped_linear), and the rows of each
  * token added up (moe_combine).
+ * The products' rows are what the matrix cores take, 16-bit or MXFP4 ones, so
+ * the hidden rows between two products of an FFN are rounded to them; rows that
+ * are to be added up can stay in fp32 (MOE_OUT_F32).
  *
  * moe_group: ids [T][k] as moe_gate writes them (an id outside [0, n_experts)
  * is no choice; the same id may come again in a row).  Rows, one per choice,
@@ -564,11 +567,13 @@ int32_t moe_grouped_path_for(const moe_grouped_desc *desc, const void *x, int64_
  * 0 <= R <= 2^24; ldx, ldw, ldo up to 2^22 (MXFP4: ldx, ldw up to 2^23, ldxs,
  * ldw_s to 2^22); with `rows`, x's rows lie within 2 GiB; a launch holds fewer
  * than 2^32 threads (n_out (R / 128 + n_groups) below 2^28 always does;
- * MOE_EUNSUPPORTED where none can).  MXFP4: n_in a multiple
- * of 128, rows of codes at multiples of 16 bytes, rows of scales at multiples
- * of 4 (MOE_EUNSUPPORTED for n_in and the scales).  16-bit elements need their
- * own alignment only; rows at multiples of 16 bytes, n_in of 8, take the
- * faster kernels.  Outputs as moe_linear's; they must not overlap inputs.
+ * MOE_EUNSUPPORTED where none can).  MXFP4: n_in a multiple of 128, rows of
+ * codes at multiples of 16 bytes, rows of scales at multiples of 4
+ * (MOE_EUNSUPPORTED for n_in and the scales); rows of another width lie in
+ * zeroed ones of such a width, since moe_mx_quantize takes row distances, and
+ * codes and scale bytes of 0 add nothing.  16-bit elements need their own
+ * alignment only; rows at multiples of 16 bytes, n_in of 8, take the faster
+ * kernels.  Outputs as moe_linear's; they must not overlap inputs.
  * Needs no workspace.
  */
 moe_status moe_grouped_linear(const moe_grouped_desc *desc, const void *x, int64_t ldx, const uint8_t *x_s, int64_t ldxs,
