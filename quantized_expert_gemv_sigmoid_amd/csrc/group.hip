@@ -16,7 +16,9 @@ namespace {
 // wave has counted of its expert so far plus the lower lanes that chose it too.
 // Up to 1024 choices in one launch (16 of 896 experts 3.4 us, a chain of loads
 // and barriers; 16 waves for them took 6.9), more in two: 32768 of 64 experts 5
-// and 7 us, 32 blocks of 1024 (8 of 4096: 6.5 and 13).
+// and 6-7 us, 32 blocks of 1024 (8 of 4096: 6.5 and 13).  The bytes are nothing
+// (0.5 MB); each launch is such a chain, the second one's with the counts of all
+// blocks in it.
 constexpr int kGroupWaves = 16;
 constexpr int kGroupThreads = kGroupWaves * 64;
 
@@ -191,9 +193,10 @@ __device__ __forceinline__ void to_f32(const Raw8 &r, int type, float (&v)[8])
 // A thread adds eight columns of a token's rows, in the order of its choices,
 // fp32 throughout; YT: the rows' type.  B rows are on the way at once; a choice
 // without a row reads one that is there and adds nothing.  Bound by memory: 4096
-// tokens of 8 rows of 2048 bf16 with a residual 29 us (5400 GB/s; four rows on
-// the way and a branch for each 45), of fp32 rows 54; one token of 16 5 us, a
-// chain of three loads.
+// tokens of 8 rows of 2048 bf16 with a residual, rows in any order, 31-33 us (5350-
+// 5100 GB/s; four rows on the way and a branch for each 45), of fp32 rows 54-57
+// (5600-5300); one token of 16 5 us, a chain of three loads (place, its weight, its
+// row) in one block.
 template <int YT, int B>
 __global__ __launch_bounds__(256) void k_group_combine(CombineParams p)
 {

@@ -195,13 +195,18 @@ constexpr GroupedKind kGroupedKinds[] = {
 // rows fell on the groups at random, which leaves some of them empty where
 // there are few rows, and a tile of each other group half full on average; and
 // with the ends of a block, since a group's product is often a short one.
-// Measured with every kernel at 20 sizes of 8 to 32768 rows, 16-bit and MXFP4,
-// ragged groups: 3% behind the best on average, 20% at most (unaligned, 4000 rows
-// of 8 x 2049 x 1025: 128 x 128 83 us, 64 x 64 68).  Both sides of some: 512 rows
-// of 64 x 2048 x 3584 64 x 32 147 us, 256 x 128 168; 4096 of 64 x 2048 x 2 x 1408
-// 256 x 128 171, 128 x 128 184, 64 x 32 232; 128 of 8 x 4096 x 4096 64 x 64 43,
-// 64 x 32 51; 16 of 896 x 1024 x 2 x 512 64 x 32 8.5, 64 x 64 9.9.  The kernels of
-// 16 rows lost at every size (16 of 896: 13 us).  Kind -1: too large for any.
+// Measured with every kernel at 36 sizes of 8 to 32768 rows in ragged groups, ten
+// of them not used in the fit: the choice is 2% behind the best on average for
+// 16-bit rows, 4% for MXFP4 ones, 5% for unaligned ones.  Furthest: MXFP4 1200 rows
+// of 16 x 640 x 2 x 512, 256 x 128 12.6 us, 64 x 64 7.9 (below one block per CU only
+// a part of a block's ends counts, which favours large tiles); MXFP4 128 rows of 8 x
+// 4096 x 4096, 64 x 32 20.6, 64 x 64 16.1; 1024 of the same in 16 bits, 128 x 128
+// 88.8, 256 x 128 70.9; unaligned 4000 of 8 x 2049 x 1025, 128 x 128 82, 64 x 64 66.
+// Both sides of some others: 512 rows of 64 x 2048 x 3584 64 x 32 146 us, 256 x 128
+// 163; 4096 of 64 x 2048 x 2 x 1408 256 x 128 158, 128 x 128 174, 64 x 32 213; 1000 of
+// 1 x 2048 x 2048 128 x 64 15.8, 64 x 64 18.6, 128 x 128 19.2; 16 of 896 x 1024 x 2 x
+// 512 64 x 32 8.5, 64 x 64 9.1.  The kernels of 16 rows lost at every size (16 of
+// 896: 13 us).  Kind -1: too large for any.
 LinearPlan grouped_plan(const GroupedParams &p, bool mx)
 {
     const bool any = !mx && !(pieces(p) && p.wstride % 8 == 0);

@@ -279,7 +279,6 @@ __device__ __forceinline__ void barrier()
 }
 
 typedef uint32_t u32x2_t __attribute__((ext_vector_type(2)));
-typedef uint16_t u16x2_t __attribute__((ext_vector_type(2)));
 
 // MXFP4: a lane's two products of a stage take neighbouring blocks, pieces 2 q
 // and 2 q + 1 of its row (16-bit rows: q and 4 + q), so that both scales come
@@ -1001,9 +1000,11 @@ __device__ __forceinline__ f32x4_t mfma_mx(V a, int sa, V b, int sb, f32x4_t c)
 // (27, 27), 2048 x 3585 x 3587 86 and 116 (74, 89).
 // MXFP4 rows: 128 bytes are 256 codes, a stage of the same bytes, and each wave
 // copies 32 rows' scales of it, 8 bytes a row, behind them: 512 x 3584 x 7168 14.2
-// us (128 x 128), 200 x 1120 x 2049 7.2 (64 x 32).  Groups: 512 rows of 64 groups x
-// 2048 x 3584 (64 x 32) 147 us, 6400 GB/s of weights, one token's eight of 128
-// experts x 3584 x 2 x 2048 36 us.
+// to 14.9 us (128 x 128; 14.5 on zeros), 200 x 1120 x 2049 7.2 (64 x 32).  Groups:
+// 512 rows of 64 groups x 2048 x 3584 (64 x 32), 55 to 58 of which have rows, 153 us,
+// 5300 to 5500 GB/s of weights from memory (a kernel that only reads: 6050 to 6400),
+// one token's eight of 128 experts x 3584 x 2 x 2048 36 us; MXFP4 ones 14.8 and
+// 4200 GB/s, where the weights are a quarter and the start of a block is not.
 template <int TN, int TM, int WN, int WT, int NST, bool MX>
 struct Tile {
     static constexpr int NW = WN * WT, THREADS = NW * 64;
@@ -1341,14 +1342,18 @@ __global__ __launch_bounds__(256) void k_linear_join(LinearParams p)
 // (32 for either pair of waves), each multiplied with the whole stage's tokens
 // in a phase of its own: quarters in a ring of five, tokens in one of two.
 // Measured beside 256 x 256 tiles, one block to a CU: 16384 rows of 64 ragged
-// groups x 3584 x 2 x 2048, SiTU, MXFP4 250 us (335); 32768 of 64 x 2048 x 2 x
-// 1408, SwiGLU, bf16 400-430 (410-440), 16384 rows of 128 groups x 2048 x 2 x
+// groups x 3584 x 2 x 2048, SiTU, MXFP4 255-275 us (335); 32768 of 64 x 2048 x 2 x
+// 1408, SwiGLU, bf16 395-430 (410-440), 16384 rows of 128 groups x 2048 x 2 x
 // 1024 247 (290); one group of 4096 x 8192 x 4096 bf16 207 (1330 TFLOP/s).  With
 // long K they are 10% behind (4096 x 7168 x 7168 MXFP4 127, 112): a wave reads
-// 1.5 times the LDS bytes per product.  Power again: the SwiGLU call takes 352
-// on zeros.  Six quarters in the ring, a higher wave priority at the products,
-// products kept in the order they are written in, and products skipped for
-// tokens past a group's end were equal or 3 to 5% slower.
+// 1.5 times the LDS bytes per product.  What the first call's 264 us are made of,
+// by leaving one thing out at a time: weights from memory 39 (one matrix for all
+// groups: 225), power 20 (zeros: 244), both 68 (196), SiTU over SwiGLU 24 (240);
+// of the second's 409: 51, 54 and 137.  The weights come at 2 to 2.5 TB/s, so a
+// block waits for them and memory does not; 161 tiles of 128 rows hold what 128
+// full ones would.  Six quarters in the ring, a higher wave priority at the
+// products, products kept in the order they are written in, and products
+// skipped for tokens past a group's end were equal or 3 to 5% slower.
 template <bool MX>
 struct Pair {
     static constexpr int QROWS = 64, TOKENS = 128, NA = 5, NB = 2;
@@ -1592,6 +1597,9 @@ __global__ __launch_bounds__(256, 2) void k_linear_pair(P p, int tn, int tt, int
 // them, 11.5 us, 4470 GB/s, from memory (the first kernel, a wave per row
 // without LDS, took 91).
 // One stage more in the ring takes the same time.
+// MXFP4 with its scales behind each stage takes 86 KB (gated 94) for eight tokens,
+// one block to a CU where 16-bit rows have two: 1 x 7168 x 7168 8.6 us for 448
+// blocks, 7.4 for the 224 of 1 x 7168 x 3584 (calls from Python).
 constexpr int kFewWaves = 8;
 
 template <bool GATED, int XP, int NST, bool MX>
