@@ -1342,7 +1342,7 @@ __global__ __launch_bounds__(256) void k_linear_join(LinearParams p)
 // (32 for either pair of waves), each multiplied with the whole stage's tokens
 // in a phase of its own: quarters in a ring of five, tokens in one of two.
 // Measured beside 256 x 256 tiles, one block to a CU: 16384 rows of 64 ragged
-// groups x 3584 x 2 x 2048, SiTU, MXFP4 255-275 us (335); 32768 of 64 x 2048 x 2 x
+// groups x 3584 x 2 x 2048, SiTU, MXFP4 247-275 us (335); 32768 of 64 x 2048 x 2 x
 // 1408, SwiGLU, bf16 395-430 (410-440), 16384 rows of 128 groups x 2048 x 2 x
 // 1024 247 (290); one group of 4096 x 8192 x 4096 bf16 207 (1330 TFLOP/s).  With
 // long K they are 10% behind (4096 x 7168 x 7168 MXFP4 127, 112): a wave reads
